@@ -288,8 +288,8 @@ def work(case):
         if case["op"] == "ln":
             return {"bytes": fwd, "flops": 9 * n}
         again = 2 * (n + n // 32) if case["save"] == "ckpt8" else ins * n * e
-        outs = 2 if ins == 2 else 1
-        return {"bytes": fwd + again + (1 + outs) * n * e + 3 * width * e + 8 * rows, "flops": 22 * n}
+        # rows: the residual's gradient is dx itself, so it costs no second write
+        return {"bytes": fwd + again + 2 * n * e + 3 * width * e + 8 * rows, "flops": 22 * n}
     out, banks = case["out"], case["banks"]
     m, wts = rows * out, banks * out * width
     bias = banks * out if case["bias"] else 0
