@@ -457,6 +457,98 @@ TM_API tm_status tm_stack_backward(const void *X, const void *dY, const tm_block
                                    const tm_shape *shape, void *dX, const tm_block_grads *grads, void *workspace,
                                    size_t workspace_bytes, void *stream);
 
+/* ---- The post-norm per-token block: layer norm, per-token linear layers, 8-bit checkpoints ------
+ * The operators of the block that [digest] 2.3.1 Eq. 5-8 and the per-token FFN with bias describe
+ * beside the pre-norm one: S = LN(Mix(X) + X); Y = LN(act(S W1^T + b1) W2^T + b2 + S), each with its
+ * backward pass, and activation checkpoints in 8 bits that the forward passes write and the backward
+ * passes read.  Shared rules: rows are [B, banks, width] unless a call says otherwise; no output may
+ * overlap an input or another output (TM_ERR_INVALID_ARG); all tensors 16-byte aligned, the fp32
+ * statistics and the exponents of a checkpoint included; gradients are written (not accumulated) in
+ * the storage dtype; sums are held in fp32 and taken in a fixed order. */
+
+/* 8-bit checkpoint of rows [rows, width].  codes [rows, width] int8; exps [rows, ceil(width / 32)]
+ * int8: the 32 values of a block of a row share the scale 2^e, e the smallest integer with
+ * max|finite value| <= 127 * 2^e, at least -126 and at most 121; code = nearest integer to value *
+ * 2^-e, ties to even, held to +-127 (which only binds above 127 * 2^121); code -128 stands for a value
+ * that is not finite and reads back as NaN. */
+typedef struct { int8_t *codes; int8_t *exps; } tm_ckpt8;
+
+/* x [rows, width] (dtype f32 or bf16) to a checkpoint, and back (exact in both dtypes).  width >= 1
+ * of any size; rows >= 1. */
+TM_API tm_status tm_checkpoint8_pack(const void *x, tm_dtype dtype, size_t rows, int width, const tm_ckpt8 *out,
+                                     void *stream);
+TM_API tm_status tm_checkpoint8_unpack(const tm_ckpt8 *in, tm_dtype dtype, size_t rows, int width, void *x,
+                                       void *stream);
+
+/* Layer norm over rows of `width`, one gain and bias [width] for all banks (NULL: ones / zeros). */
+typedef struct { int banks, width; const void *gain, *bias; } tm_layer_norm_w;
+
+/* y = (z - mean) * rstd * gain + bias with z = x_row + residual_row, mean = mean(z), rstd =
+ * 1 / sqrt(mean((z - mean)^2) + eps) of each row.
+ * x: rows, or with TM_LAYOUT_MIXED a token tensor [B, T, D] whose Mix rows are taken (banks = H, width
+ * = T * D / H); residual (NULL: none) and y are rows [B, banks, width] in both layouts, so with T = H
+ * and residual = X this is the token mixing LN(Mix(X) + X) of [digest] Eq. 5-8.
+ * mean_opt, rstd_opt [B, banks] fp32 and save_opt, the checkpoint of z over B * banks rows: what the
+ * backward pass needs (each may be NULL).
+ * width <= 16384; any width in the row layout, head widths that are multiples of 8 (bf16) or 4 (f32)
+ * in the mixed one (others TM_ERR_UNSUPPORTED). */
+TM_API tm_status tm_layer_norm(const void *x, const void *residual, tm_layout layout, const tm_shape *shape,
+                               const tm_layer_norm_w *w, void *y, float *mean_opt, float *rstd_opt,
+                               const tm_ckpt8 *save_opt, void *stream);
+
+/* Gradients of gain and bias [width] (each may be NULL: not wanted). */
+typedef struct { void *dgain, *dbias; } tm_layer_norm_grads;
+
+TM_API size_t tm_layer_norm_backward_workspace_bytes(const tm_shape *shape, tm_layout layout,
+                                                     const tm_layer_norm_w *w);
+
+/* For the gradient dy of y (rows): dn = dy * gain, n = (z - mean) * rstd,
+ *   dz = rstd (dn - mean(dn) - n mean(dn n)), dgain = sum over rows of dy n, dbias = sum of dy.
+ * z comes from `saved` (the forward's checkpoint; x and residual are then not read and may be NULL) or,
+ * with saved NULL, from x and residual as in the forward.  mean, rstd: the forward's.
+ *   row layout:   dx = dz, which is the residual's gradient too (dresidual_opt and residual_is_x NULL / 0).
+ *   mixed layout: dx [B, T, D] = Revert(dz); dresidual_opt (may be NULL) = dz.  residual_is_x != 0 says
+ *                 that x and the residual are one tensor X (T = H): dx = dz + Revert(dz), its whole
+ *                 gradient, dresidual_opt NULL; needs T * D * 4 <= 220 KB and width <= 1024. */
+TM_API tm_status tm_layer_norm_backward(const void *x, const void *residual, const tm_ckpt8 *saved, const float *mean,
+                                        const float *rstd, const void *dy, tm_layout layout, const tm_shape *shape,
+                                        const tm_layer_norm_w *w, int residual_is_x, void *dx, void *dresidual_opt,
+                                        const tm_layer_norm_grads *grads, void *workspace, size_t workspace_bytes,
+                                        void *stream);
+
+/* Activations of the per-token linear layer: none, relu, gelu (z Phi(z), Phi the normal distribution
+ * function), silu (z / (1 + e^-z)). */
+typedef enum { TM_ACT_NONE = 0, TM_ACT_RELU = 1, TM_ACT_GELU = 2, TM_ACT_SILU = 3 } tm_act;
+
+/* Per-token linear layer: one matrix w [banks, out, width] and bias [banks, out] (NULL: none) per bank.
+ * banks = 1 shares one matrix among all rows. */
+typedef struct { int banks, width, out; tm_act act; const void *w, *bias; } tm_linear_w;
+
+/* y[b, bank] = act(z) + residual[b, bank], z = x[b, bank] . w[bank]^T + bias[bank];
+ * x [B, banks, width], residual (NULL: none) and y [B, banks, out].  shape: B, dtype (T, D, H only have
+ * to be a valid shape).  For the backward pass of an activation the pre-activation z is kept either
+ * whole (z_opt [B, banks, out], the storage dtype) or as a checkpoint (save_opt, B * banks rows); both
+ * may be NULL, both given is TM_ERR_INVALID_ARG, as is either with TM_ACT_NONE.
+ * bf16: width and out multiples of 8 (tensor cores, fp32 accumulation); f32: any sizes (CUDA cores),
+ * banks and B / 64 up to 65535.  Others TM_ERR_UNSUPPORTED. */
+TM_API tm_status tm_pertoken_linear(const void *x, const void *residual, const tm_shape *shape, const tm_linear_w *w,
+                                    void *y, void *z_opt, const tm_ckpt8 *save_opt, void *stream);
+
+/* dw [banks, out, width], db [banks, out] (each may be NULL: not wanted). */
+typedef struct { void *dw, *db; } tm_linear_grads;
+
+TM_API size_t tm_pertoken_linear_backward_workspace_bytes(const tm_shape *shape, const tm_linear_w *w);
+
+/* For the gradient dy of y [B, banks, out]: dz = dy * act'(z),
+ *   dx = dz w + dx_add (NULL: none; [B, banks, width]), dw = dz^T x, db = sum over b of dz.
+ * z or saved: what the forward kept (exactly one of them with an activation; neither is read without
+ * one).  The residual's gradient is dy itself.  dx may be NULL (not wanted).  dz is rounded to the
+ * storage dtype before the two products. */
+TM_API tm_status tm_pertoken_linear_backward(const void *x, const void *dy, const void *z, const tm_ckpt8 *saved,
+                                             const void *dx_add, const tm_shape *shape, const tm_linear_w *w, void *dx,
+                                             const tm_linear_grads *grads, void *workspace, size_t workspace_bytes,
+                                             void *stream);
+
 /* Per-kernel timing of the library's own launches (tracing). */
 typedef struct {
     char name[48];       /* kernel family, e.g. "gemm_swiglu" */

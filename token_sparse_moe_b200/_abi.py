@@ -12,6 +12,7 @@ TM_OK, TM_ERR_INVALID_ARG, TM_ERR_UNSUPPORTED, TM_ERR_WORKSPACE, TM_ERR_CUDA, TM
 TM_F32, TM_BF16 = 0, 1
 TM_LAYOUT_ROWS, TM_LAYOUT_MIXED = 0, 1
 TM_TP_TOKEN_SHARD, TM_TP_HEAD_SHARD = 0, 1
+TM_ACT_NONE, TM_ACT_RELU, TM_ACT_GELU, TM_ACT_SILU = range(4)
 
 # Every entry point declared in include/tm.h (the CPU test checks the library exports each one).
 EXPORTS = ["tm_status_string", "tm_version", "tm_sublayer_workspace_bytes", "tm_route_workspace_bytes",
@@ -26,7 +27,9 @@ EXPORTS = ["tm_status_string", "tm_version", "tm_sublayer_workspace_bytes", "tm_
            "tm_block_backward_workspace_bytes", "tm_block_backward", "tm_stack_backward_workspace_bytes",
            "tm_stack_backward", "tm_last_device_error_site", "tm_set_wait_limit_ns", "tm_selftest_wait",
            "tm_selftest_bucket_scatter", "tm_sublayer_fp8_workspace_bytes", "tm_sublayer_forward_fp8",
-           "tm_sparse_pertoken_moe_fp8", "tm_tp_exchange_layout"]
+           "tm_sparse_pertoken_moe_fp8", "tm_tp_exchange_layout", "tm_checkpoint8_pack", "tm_checkpoint8_unpack",
+           "tm_layer_norm", "tm_layer_norm_backward_workspace_bytes", "tm_layer_norm_backward", "tm_pertoken_linear",
+           "tm_pertoken_linear_backward_workspace_bytes", "tm_pertoken_linear_backward"]
 
 
 class tm_shape(ctypes.Structure):
@@ -80,6 +83,27 @@ class tm_swiglu_grads(ctypes.Structure):
 
 class tm_block_grads(ctypes.Structure):
     _fields_ = [("mix", tm_swiglu_grads), ("rev", tm_swiglu_grads)]
+
+
+class tm_ckpt8(ctypes.Structure):
+    _fields_ = [("codes", c_void_p), ("exps", c_void_p)]
+
+
+class tm_layer_norm_w(ctypes.Structure):
+    _fields_ = [("banks", c_int), ("width", c_int), ("gain", c_void_p), ("bias", c_void_p)]
+
+
+class tm_layer_norm_grads(ctypes.Structure):
+    _fields_ = [("dgain", c_void_p), ("dbias", c_void_p)]
+
+
+class tm_linear_w(ctypes.Structure):
+    _fields_ = [("banks", c_int), ("width", c_int), ("out", c_int), ("act", c_int), ("w", c_void_p),
+                ("bias", c_void_p)]
+
+
+class tm_linear_grads(ctypes.Structure):
+    _fields_ = [("dw", c_void_p), ("db", c_void_p)]
 
 
 class tm_kernel_time(ctypes.Structure):
@@ -140,6 +164,18 @@ _SIGS = {
     "tm_stack_backward_workspace_bytes": (c_size_t, [POINTER(tm_shape), POINTER(tm_block), c_int, c_int]),
     "tm_stack_backward": (c_int, [_P, _P, POINTER(tm_block), c_int, c_int, POINTER(tm_shape), _P,
                                   POINTER(tm_block_grads), _P, c_size_t, _P]),
+    "tm_checkpoint8_pack": (c_int, [_P, c_int, c_size_t, c_int, POINTER(tm_ckpt8), _P]),
+    "tm_checkpoint8_unpack": (c_int, [POINTER(tm_ckpt8), c_int, c_size_t, c_int, _P, _P]),
+    "tm_layer_norm": (c_int, [_P, _P, c_int, POINTER(tm_shape), POINTER(tm_layer_norm_w), _P, _P, _P,
+                              POINTER(tm_ckpt8), _P]),
+    "tm_layer_norm_backward_workspace_bytes": (c_size_t, [POINTER(tm_shape), c_int, POINTER(tm_layer_norm_w)]),
+    "tm_layer_norm_backward": (c_int, [_P, _P, POINTER(tm_ckpt8), _P, _P, _P, c_int, POINTER(tm_shape),
+                                       POINTER(tm_layer_norm_w), c_int, _P, _P, POINTER(tm_layer_norm_grads), _P,
+                                       c_size_t, _P]),
+    "tm_pertoken_linear": (c_int, [_P, _P, POINTER(tm_shape), POINTER(tm_linear_w), _P, _P, POINTER(tm_ckpt8), _P]),
+    "tm_pertoken_linear_backward_workspace_bytes": (c_size_t, [POINTER(tm_shape), POINTER(tm_linear_w)]),
+    "tm_pertoken_linear_backward": (c_int, [_P, _P, _P, POINTER(tm_ckpt8), _P, POINTER(tm_shape), POINTER(tm_linear_w),
+                                            _P, POINTER(tm_linear_grads), _P, c_size_t, _P]),
 }
 
 _lib = None

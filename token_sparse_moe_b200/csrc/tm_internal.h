@@ -134,6 +134,33 @@ cudaError_t launch_swiglu_bwd(const void* Gp, const void* Up, const void* dH, si
 cudaError_t launch_rms_bwd(const void* x, const void* dN, const float* inv_rms, const void* add0, const void* add1,
                            const void* add2, RowMap m, int B, void* dx, cudaStream_t st);
 
+// ---- post-norm block (tm_ckpt8.cu, tm_norm.cu, tm_linear.cu) ------------------------
+struct NormParams;
+struct LinParams;
+struct SimtLin;
+// 8-bit checkpoints: pack x -> codes, exps, or unpack into x
+cudaError_t launch_ckpt8(bool pack, int dtype, void* x, void* codes, void* exps, long long rows, int width, int sms,
+                         cudaStream_t st);
+int norm_max_width();
+bool ln_self_supported(int H, int W);
+size_t ln_part_floats(long long nrows, int W, int sms);
+cudaError_t launch_ln_fwd(int dtype, const NormParams& p, cudaStream_t st);
+cudaError_t launch_ln_bwd(int dtype, const NormParams& p, bool self, void* dgain, void* dbias, int sms,
+                          cudaStream_t st);
+cudaError_t launch_linear_simt(const SimtLin& p, cudaStream_t st);
+cudaError_t launch_linear_fwd(int bn, int act, int save, const CUtensorMap& a, const CUtensorMap& b,
+                              const CUtensorMap& o, const CUtensorMap& z, const LinParams& p, int sms, cudaStream_t st);
+cudaError_t launch_linear_dx(int bn, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
+                             const LinParams& p, int sms, cudaStream_t st);
+cudaError_t launch_linear_dw(int bn, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
+                             const LinParams& p, int sms, cudaStream_t st);
+// out[i] = sum over r < R of part[r][i]
+cudaError_t launch_sum_parts(int dtype, const float* part, int R, long long n, void* out, cudaStream_t st);
+int act_bwd_chunks(int dtype, int B, long long cols, int N, int sms);
+// dz = dy act'(z) over [B, cols] (z whole or codes / exps) and its column sums part [chunks][cols]
+cudaError_t launch_act_bwd(int dtype, const void* dy, const void* z, const int8_t* codes, const int8_t* exps, int act,
+                           int B, long long cols, int N, int chunks, void* dz, float* part, cudaStream_t st);
+
 // fp32 CUDA-core grouped GEMM with the same tile space and epilogues as the tcgen05 one.
 // A is x (gathered through amap) when epi == EPI_SWIGLU, else hidden rows [positions, K].
 struct SimtGemmArgs {

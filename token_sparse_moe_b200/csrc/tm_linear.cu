@@ -1,0 +1,327 @@
+// tm_linear.cu -- the per-token linear layer beside its tensor-core contractions (tm_linear.cuh): the
+// activation's derivative with the bias gradient's column sums, the sums of partial results, the fp32
+// form of the contractions on CUDA cores, and the launchers.
+#include <atomic>
+
+#include "tm_linear.cuh"
+#include "tm_internal.h"
+
+namespace tml {
+
+// ------------------------------------------------------------------ activations in fp32
+// The fp32 path calls the CUDA math functions; bf16 results take the short forms of tm_linear.cuh.
+__device__ __forceinline__ float act_f32(int act, float z) {
+    if (act == LIN_RELU) return max_nan(z, 0.f);
+    if (act == LIN_GELU) return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    if (act == LIN_SILU) return z / (1.f + expf(-z));
+    return z;
+}
+// act'(z): gelu' = Phi(z) + z phi(z); silu' = s (1 + z (1 - s)), s = sigmoid(z)
+template <typename T>
+__device__ __forceinline__ float act_slope(int act, float z) {
+    if (act == LIN_RELU) return z > 0.f ? 1.f : (z == z ? 0.f : z);   // NaN stays
+    if (act == LIN_GELU) {
+        if constexpr (sizeof(T) == 4)
+            return fmaf(z * 0.39894228040143268f, expf(-0.5f * z * z), 0.5f * erfcf(-0.70710678118654752f * z));
+        const float a = fminf(fabsf(z), 16.f);
+        const float q = gauss_tail2(make_float2(a, a)).x;
+        const float cdf = z >= 0.f ? 1.f - q : q;
+        return fmaf(z * 0.39894228040143268f, ex2_approx(-0.72134752044448170f * (z * z)), cdf);
+    }
+    if (act == LIN_SILU) {
+        const float s = sizeof(T) == 4 ? 1.f / (1.f + expf(-z))
+                                       : rcp_approx(1.f + ex2_approx(-1.4426950408889634f * z));
+        return s * fmaf(z, 1.f - s, 1.f);
+    }
+    return 1.f;
+}
+
+// ------------------------------------------------------------------ dz = dy act'(z), db = sum over b of dz
+// dy, z, dz are [B, cols] with cols = banks * N; a thread owns V columns and walks down its block's
+// rows; the sums over a block's rows go to part [gridDim.y][cols] (in a fixed order).  SRC: what z is
+// read from.  dz may be NULL (no activation: dz is dy, only the sums are wanted).
+enum ZSrc : int { Z_NONE = 0, Z_FULL = 1, Z_CK8 = 2 };
+constexpr int kActX = 64, kActY = 4, kActU = 4;
+
+template <typename T, int V, int SRC>
+__global__ void __launch_bounds__(kActX * kActY)
+    act_bwd_kernel(const T* __restrict__ dy, const T* __restrict__ z, const int8_t* __restrict__ codes,
+                   const int8_t* __restrict__ exps, int act, int B, long long cols, int N, int nblk, int rows_per,
+                   T* __restrict__ dz, float* __restrict__ part) {
+    __shared__ float sm[kActY][kActX][V];
+    const int tx = threadIdx.x % kActX, ty = threadIdx.x / kActX;
+    const long long c = ((long long)blockIdx.x * kActX + tx) * V;
+    const bool in = c < cols;
+    const long long bank = in ? c / N : 0;
+    const int n = in ? (int)(c - bank * N) : 0;
+    const long long erow = cols / N * nblk;              // exponents per b
+    const long long eoff = bank * nblk + n / kCk8Block;
+    const int b0 = blockIdx.y * rows_per, b1 = min(B, b0 + rows_per);
+    float s[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) s[k] = 0.f;
+    if (in) {
+        for (int b = b0 + ty; b < b1; b += kActY * kActU) {
+            Pack<T, V> dw[kActU], zw[kActU];
+            uint32_t q[kActU][(V + 3) / 4];
+            int e[kActU];
+#pragma unroll
+            for (int u = 0; u < kActU; ++u) {
+                const int r = b + u * kActY;
+                if (r >= b1) continue;
+                dw[u].load(dy + r * cols + c);
+                if constexpr (SRC == Z_FULL) zw[u].load(z + r * cols + c);
+                if constexpr (SRC == Z_CK8) {
+                    ck8_load<V>(codes + r * cols + c, q[u]);
+                    e[u] = __ldg(exps + r * erow + eoff);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kActU; ++u) {
+                const int r = b + u * kActY;
+                if (r >= b1) continue;
+                float d[V], zv[V];
+                dw[u].get(d);
+                if constexpr (SRC != Z_NONE) {
+                    if constexpr (SRC == Z_FULL) zw[u].get(zv);
+                    else ck8_values<V>(q[u], ck8_scale(e[u]), zv);
+#pragma unroll
+                    for (int k = 0; k < V; ++k) d[k] *= act_slope<T>(act, zv[k]);
+                    Pack<T, V>::store(dz + r * cols + c, d);
+                }
+#pragma unroll
+                for (int k = 0; k < V; ++k) s[k] += d[k];
+            }
+        }
+    }
+    if (!part) return;
+#pragma unroll
+    for (int k = 0; k < V; ++k) sm[ty][tx][k] = s[k];
+    __syncthreads();
+    if (ty == 0 && in) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            float t = 0.f;
+#pragma unroll
+            for (int y = 0; y < kActY; ++y) t += sm[y][tx][k];
+            part[blockIdx.y * cols + c + k] = t;
+        }
+    }
+}
+
+// out[i] = sum over r < R of part[r][i], in order
+template <typename T>
+__global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict__ part, int R, long long n,
+                                                        T* __restrict__ out) {
+    const bool vec = (n & 3) == 0;
+    const long long n4 = vec ? n / 4 : n;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n4; i += (long long)gridDim.x * 256) {
+        if (vec) {
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int r = 0; r < R; ++r) {
+                const float4 w = __ldg(reinterpret_cast<const float4*>(part + r * n) + i);
+                s.x += w.x; s.y += w.y; s.z += w.z; s.w += w.w;
+            }
+            from_f(s.x, out + 4 * i);
+            from_f(s.y, out + 4 * i + 1);
+            from_f(s.z, out + 4 * i + 2);
+            from_f(s.w, out + 4 * i + 3);
+        } else {
+            float s = 0.f;
+            for (int r = 0; r < R; ++r) s += __ldg(part + r * n + i);
+            from_f(s, out + i);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ fp32 contractions
+// D[g][m][n] = sum_k A[g][m][k] B[g][n][k] with every stride given, 64 x 64 tiles, slabs of 16, 4 x 4
+// outputs a thread; the forward's epilogue as in tm_linear.cuh.
+struct SimtLin {
+    const float *a, *b, *bias, *add;
+    float *d, *z;
+    int8_t *codes, *exps;
+    long long ag, am, ak, bg, bn, bk, dg, dm;   // element strides (D's columns are contiguous)
+    int groups, M, N, K, act, nblk;
+};
+
+__global__ void __launch_bounds__(256) linear_simt_kernel(const SimtLin p) {
+    __shared__ float sa[16][68], sb[16][68];
+    const int g = blockIdx.z, m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const float* A = p.a + g * p.ag;
+    const float* Bm = p.b + g * p.bg;
+    float acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    for (int k0 = 0; k0 < p.K; k0 += 16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // the contiguous index runs across the threads
+            const int e = threadIdx.x + 256 * i;
+            const int ak = p.ak == 1 ? e & 15 : e >> 6, am = p.ak == 1 ? e >> 4 : e & 63;
+            const int bk = p.bk == 1 ? e & 15 : e >> 6, bn = p.bk == 1 ? e >> 4 : e & 63;
+            sa[ak][am] = (m0 + am < p.M && k0 + ak < p.K) ? __ldg(A + (m0 + am) * p.am + (k0 + ak) * p.ak) : 0.f;
+            sb[bk][bn] = (n0 + bn < p.N && k0 + bk < p.K) ? __ldg(Bm + (n0 + bn) * p.bn + (k0 + bk) * p.bk) : 0.f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            float av[4], bv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) { av[i] = sa[k][ty * 4 + i]; bv[i] = sb[k][tx * 4 + i]; }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int m = m0 + ty * 4 + i, n = n0 + tx * 4;
+        const bool row_in = m < p.M;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (p.bias && n + j < p.N) acc[i][j] += __ldg(p.bias + (long long)g * p.N + n + j);
+        const long long r = (long long)m * p.groups + g;      // row of the forward's rows
+        if (p.codes) {
+            uint32_t q[1];
+            const int e = ck8_quantize<4, 8>(acc[i], q);      // a block of 32 columns: 8 lanes
+            if (row_in) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n + j < p.N) p.codes[r * p.N + n + j] = (int8_t)(q[0] >> (8 * j));
+                if ((n & 31) == 0 && n < p.N) p.exps[r * p.nblk + (n >> 5)] = (int8_t)e;
+            }
+        }
+        if (!row_in) continue;
+        const long long o = g * p.dg + m * p.dm + n;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (n + j >= p.N) break;
+            if (p.z) p.z[o + j] = acc[i][j];
+            float y = act_f32(p.act, acc[i][j]);
+            if (p.add) y += __ldg(p.add + o + j);
+            p.d[o + j] = y;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ launchers
+cudaError_t launch_linear_simt(const SimtLin& p, cudaStream_t st) {
+    ProfileScope ps_("linear_f32", st);
+    const dim3 grid((p.N + 63) / 64, (p.M + 63) / 64, p.groups);
+    linear_simt_kernel<<<grid, 256, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <int BN, bool A_MN, bool B_MN, int ACT, int SAVE, bool F32OUT>
+static cudaError_t launch_linear_one(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
+                                     const CUtensorMap& z, const LinParams& p, int sms, cudaStream_t st) {
+    using C = LinCfg<BN, SAVE>;
+    auto kern = linear_gemm_kernel<BN, A_MN, B_MN, ACT, SAVE, F32OUT>;
+    static std::atomic<bool> configured[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
+    }
+    const long long tiles = (long long)p.groups * p.splits * p.mt * p.nt;
+    ProfileScope ps_(A_MN ? "linear_dw" : B_MN ? "linear_dx" : "linear", st);
+    kern<<<(int)(tiles < sms ? tiles : sms), C::NTHREADS, C::SMEM_BYTES, st>>>(a, b, o, z, p);
+    return cudaGetLastError();
+}
+
+template <int BN>
+static cudaError_t launch_linear_fwd_bn(int act, int save, const CUtensorMap& a, const CUtensorMap& b,
+                                        const CUtensorMap& o, const CUtensorMap& z, const LinParams& p, int sms,
+                                        cudaStream_t st) {
+    if (act == LIN_NONE)
+        return launch_linear_one<BN, false, false, LIN_NONE, LIN_KEEP_NOTHING, false>(a, b, o, z, p, sms, st);
+#define X(ACT_, SAVE_) \
+    if (act == ACT_ && save == SAVE_) \
+        return launch_linear_one<BN, false, false, ACT_, SAVE_, false>(a, b, o, z, p, sms, st);
+    X(LIN_RELU, LIN_KEEP_NOTHING) X(LIN_RELU, LIN_KEEP_FULL) X(LIN_RELU, LIN_KEEP_CK8)
+    X(LIN_GELU, LIN_KEEP_NOTHING) X(LIN_GELU, LIN_KEEP_FULL) X(LIN_GELU, LIN_KEEP_CK8)
+    X(LIN_SILU, LIN_KEEP_NOTHING) X(LIN_SILU, LIN_KEEP_FULL) X(LIN_SILU, LIN_KEEP_CK8)
+#undef X
+    return cudaErrorInvalidValue;
+}
+
+// bn: 256 or 128 columns a tile
+cudaError_t launch_linear_fwd(int bn, int act, int save, const CUtensorMap& a, const CUtensorMap& b,
+                              const CUtensorMap& o, const CUtensorMap& z, const LinParams& p, int sms,
+                              cudaStream_t st) {
+    return bn == 256 ? launch_linear_fwd_bn<256>(act, save, a, b, o, z, p, sms, st)
+                     : launch_linear_fwd_bn<128>(act, save, a, b, o, z, p, sms, st);
+}
+cudaError_t launch_linear_dx(int bn, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
+                             const LinParams& p, int sms, cudaStream_t st) {
+    return bn == 256 ? launch_linear_one<256, false, true, LIN_NONE, LIN_KEEP_NOTHING, false>(a, b, o, o, p, sms, st)
+                     : launch_linear_one<128, false, true, LIN_NONE, LIN_KEEP_NOTHING, false>(a, b, o, o, p, sms, st);
+}
+// p.splits > 1: fp32 partial sums through o
+cudaError_t launch_linear_dw(int bn, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
+                             const LinParams& p, int sms, cudaStream_t st) {
+    if (p.splits > 1)
+        return bn == 256 ? launch_linear_one<256, true, true, LIN_NONE, LIN_KEEP_NOTHING, true>(a, b, o, o, p, sms, st)
+                         : launch_linear_one<128, true, true, LIN_NONE, LIN_KEEP_NOTHING, true>(a, b, o, o, p, sms, st);
+    return bn == 256 ? launch_linear_one<256, true, true, LIN_NONE, LIN_KEEP_NOTHING, false>(a, b, o, o, p, sms, st)
+                     : launch_linear_one<128, true, true, LIN_NONE, LIN_KEEP_NOTHING, false>(a, b, o, o, p, sms, st);
+}
+
+cudaError_t launch_sum_parts(int dtype, const float* part, int R, long long n, void* out, cudaStream_t st) {
+    ProfileScope ps_("sum_parts", st);
+    const long long per = (n & 3) == 0 ? n / 4 : n;
+    const long long grid = (per + 255) / 256 < 148 * 16 ? (per + 255) / 256 : 148 * 16;
+    if (dtype == 1) sum_parts_kernel<__nv_bfloat16><<<(int)grid, 256, 0, st>>>(part, R, n, (__nv_bfloat16*)out);
+    else sum_parts_kernel<float><<<(int)grid, 256, 0, st>>>(part, R, n, (float*)out);
+    return cudaGetLastError();
+}
+
+// Row chunks of the derivative pass: enough blocks for every SM several times over, at least 16 rows
+// each, at most 64 partial sums per column.
+int act_bwd_chunks(int dtype, int B, long long cols, int N, int sms) {
+    const int V = dtype == 1 ? 8 : (N % 4 == 0 ? 4 : 1);
+    const long long gx = (cols / V + kActX - 1) / kActX;
+    long long r = (8LL * sms + gx - 1) / gx;
+    if (r > (B + 15) / 16) r = (B + 15) / 16;
+    if (r > 64) r = 64;
+    return (int)(r < 1 ? 1 : r);
+}
+
+template <typename T, int V>
+static void launch_act_bwd_v(int src, const void* dy, const void* z, const int8_t* codes, const int8_t* exps, int act,
+                             int B, long long cols, int N, int chunks, void* dz, float* part, cudaStream_t st) {
+    const dim3 grid((unsigned)((cols / V + kActX - 1) / kActX), chunks);
+    const int per = (B + chunks - 1) / chunks;
+    const int nblk = (N + kCk8Block - 1) / kCk8Block;
+#define X(SRC_)                                                                                              \
+    if (src == SRC_)                                                                                         \
+        act_bwd_kernel<T, V, SRC_><<<grid, kActX * kActY, 0, st>>>((const T*)dy, (const T*)z, codes, exps, act, B, \
+                                                                   cols, N, nblk, per, (T*)dz, part);
+    X(Z_NONE) X(Z_FULL) X(Z_CK8)
+#undef X
+}
+
+cudaError_t launch_act_bwd(int dtype, const void* dy, const void* z, const int8_t* codes, const int8_t* exps, int act,
+                           int B, long long cols, int N, int chunks, void* dz, float* part, cudaStream_t st) {
+    ProfileScope ps_("act_bwd", st);
+    const int src = act == LIN_NONE ? Z_NONE : (codes ? Z_CK8 : Z_FULL);
+    if (dtype == 1)
+        launch_act_bwd_v<__nv_bfloat16, 8>(src, dy, z, codes, exps, act, B, cols, N, chunks, dz, part, st);
+    else if (N % 4 == 0)
+        launch_act_bwd_v<float, 4>(src, dy, z, codes, exps, act, B, cols, N, chunks, dz, part, st);
+    else
+        launch_act_bwd_v<float, 1>(src, dy, z, codes, exps, act, B, cols, N, chunks, dz, part, st);
+    return cudaGetLastError();
+}
+
+}  // namespace tml
