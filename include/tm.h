@@ -462,8 +462,8 @@ TM_API tm_status tm_stack_backward(const void *X, const void *dY, const tm_block
  * beside the pre-norm one: S = LN(Mix(X) + X); Y = LN(act(S W1^T + b1) W2^T + b2 + S), each with its
  * backward pass, and activation checkpoints in 8 bits that the forward passes write and the backward
  * passes read.  Shared rules: rows are [B, banks, width] unless a call says otherwise; no output may
- * overlap an input or another output (TM_ERR_INVALID_ARG); all tensors 16-byte aligned, the fp32
- * statistics and the exponents of a checkpoint included; gradients are written (not accumulated) in
+ * overlap an input or another output (TM_ERR_INVALID_ARG); all tensors 16-byte aligned (the fp32
+ * statistics of the layer norm 4-byte); gradients are written (not accumulated) in
  * the storage dtype; sums are held in fp32 and taken in a fixed order. */
 
 /* 8-bit checkpoint of rows [rows, width].  codes [rows, width] int8; exps [rows, ceil(width / 32)]

@@ -838,119 +838,133 @@ class BlockBackwardRunner:
 
 # ------------------------------------------------------------------ the post-norm per-token block
 # Layer norm, per-token linear layers and 8-bit activation checkpoints.  These calls check every
-# tensor's shape, dtype and device against the first argument's (ValueError, nothing launched), and
-# allocate what they return, and their workspace, on the stream they run on.
-_byref = ctypes.byref
+# tensor's shape, dtype, layout and device against the first argument's (ValueError, nothing launched),
+# and allocate what they return, and their workspace, on the stream they run on.  On small inputs the
+# host side is most of a call, so an argument is checked and turned into its address in one step.
 _ACTS = {"none": A.TM_ACT_NONE, "relu": A.TM_ACT_RELU, "gelu": A.TM_ACT_GELU, "silu": A.TM_ACT_SILU}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _expect(name: str, t: Optional[torch.Tensor], shape_, dtype, device) -> None:
-    if t is not None and (t.shape != shape_ or t.dtype != dtype or t.device != device):
-        raise ValueError(f"{name}: expected {tuple(shape_)} {dtype} on {device}, got {tuple(t.shape)} {t.dtype} on "
-                         f"{t.device}")
+def _arg(name: str, t: Optional[torch.Tensor], shape_, dtype, dev: int) -> Optional[int]:
+    """Address of an argument (None: absent) that has to be a dense tensor of this shape and dtype on
+    CUDA device `dev`."""
+    if t is None:
+        return None
+    if t.shape != shape_ or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {tuple(shape_)} {dtype} tensor on cuda:{dev}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device} with strides {t.stride()}")
+    return t.data_ptr()
 
 
-def _lead(name: str, t: torch.Tensor, dims: int) -> None:
-    """The argument that the others are checked against: a float tensor on the current device (the
-    library launches there)."""
-    if t.dim() != dims or t.dtype not in _DT:
-        raise ValueError(f"{name}: expected a {dims}-dimensional float32 or bfloat16 tensor, got {tuple(t.shape)} "
-                         f"{t.dtype}")
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+def _lead(name: str, t: torch.Tensor, dims: Optional[int] = None) -> int:
+    """CUDA device of the argument that the others are checked against: it has to be the current one
+    (the library launches there)."""
+    if t.dtype not in _DT or t.dim() < 1 or (dims is not None and t.dim() != dims):
+        raise ValueError(f"{name}: expected a {'' if dims is None else f'{dims}-dimensional '}float32 or bfloat16 "
+                         f"tensor, got {tuple(t.shape)} {t.dtype}")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"libtm takes device tensors; got {name} on {t.device}")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _stream_of(stream, dev: int) -> int:
+    if stream is None:
+        return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 class _on:
-    """Allocates on the stream that the call runs on (None: the current one), so that a workspace
-    given back at the call's return is not reused ahead of its kernels by another stream."""
+    """Allocates on the stream that the call runs on, so that a workspace given back at the call's
+    return is not reused ahead of its kernels by another stream."""
     __slots__ = ("ctx",)
 
     def __init__(self, stream):
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream))
-        self.ctx = None if stream is None else torch.cuda.stream(stream)
+        self.ctx = torch.cuda.stream(stream)
 
     def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
+        self.ctx.__enter__()
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        self.ctx.__exit__(*exc)
 
 
-@dataclass
 class Checkpoint8:
     """Rows [..., width] in 8 bits: int8 codes of the same shape, int8 exponents [..., ceil(width / 32)],
     and the dtype they came from."""
-    codes: torch.Tensor
-    exps: torch.Tensor
-    dtype: torch.dtype
+    __slots__ = ("codes", "exps", "dtype")
+
+    def __init__(self, codes: torch.Tensor, exps: torch.Tensor, dtype: torch.dtype):
+        self.codes, self.exps, self.dtype = codes, exps, dtype
 
     @staticmethod
-    def empty(shape_, dtype, device) -> "Checkpoint8":
-        n = (shape_[-1] + 31) // 32
-        return Checkpoint8(torch.empty(shape_, dtype=torch.int8, device=device),
-                           torch.empty((*shape_[:-1], n), dtype=torch.int8, device=device), dtype)
+    def like(x: torch.Tensor, shape_) -> "Checkpoint8":
+        """Uninitialised, for rows of this shape and x's dtype on x's device."""
+        return Checkpoint8(x.new_empty(shape_, dtype=torch.int8),
+                           x.new_empty((*shape_[:-1], (shape_[-1] + 31) // 32), dtype=torch.int8), x.dtype)
 
-    def c(self) -> A.tm_ckpt8:
-        return A.tm_ckpt8(_p(self.codes), _p(self.exps))
-
-    def expect(self, name: str, shape_, device) -> None:
-        _expect(name + " codes", self.codes, shape_, torch.int8, device)
-        _expect(name + " exponents", self.exps, (*shape_[:-1], (shape_[-1] + 31) // 32), torch.int8, device)
+    def c(self, name: str, shape_, dev: int) -> A.tm_ckpt8:
+        """The C descriptor, the tensors checked."""
+        return A.tm_ckpt8(_arg(name + " codes", self.codes, shape_, torch.int8, dev),
+                          _arg(name + " exponents", self.exps, (*shape_[:-1], (shape_[-1] + 31) // 32), torch.int8, dev))
 
 
 def checkpoint8_pack(x: torch.Tensor, out: Optional[Checkpoint8] = None, stream=None) -> Checkpoint8:
     """tm_checkpoint8_pack: the rows of x (any leading axes) as int8 codes with one power-of-two scale
     per 32 values."""
-    _lead("x", x, max(x.dim(), 1))
-    with _on(stream):
-        if out is None:
-            out = Checkpoint8.empty(x.shape, x.dtype, x.device)
-        else:
-            out.expect("out", x.shape, x.device)
-            out.dtype = x.dtype
-        width = x.shape[-1]
-        A.check(lib().tm_checkpoint8_pack(_p(x), _DT[x.dtype], x.numel() // max(width, 1), width, _byref(out.c()),
-                                          _s(stream)), "tm_checkpoint8_pack")
+    if stream is not None:
+        with _on(stream):
+            return checkpoint8_pack(x, out)
+    dev = _lead("x", x)
+    shape_ = x.shape
+    if out is None:
+        out = Checkpoint8.like(x, shape_)
+    out.dtype = x.dtype
+    width = shape_[-1]
+    st = A.load().tm_checkpoint8_pack(_arg("x", x, shape_, x.dtype, dev), _DT[x.dtype], x.numel() // max(width, 1), width,
+                                      out.c("out", shape_, dev), _stream_of(None, dev))
+    if st:
+        A.check(st, "tm_checkpoint8_pack")
     return out
 
 
 def checkpoint8_unpack(ck: Checkpoint8, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """tm_checkpoint8_unpack: the rows that a checkpoint stands for, in its dtype."""
+    if stream is not None:
+        with _on(stream):
+            return checkpoint8_unpack(ck, out)
     codes = ck.codes
-    ck.expect("checkpoint", codes.shape, codes.device)
-    with _on(stream):
-        if out is None:
-            out = torch.empty(codes.shape, dtype=ck.dtype, device=codes.device)
-        _lead("out", out, max(codes.dim(), 1))
-        _expect("out", out, codes.shape, out.dtype, codes.device)
-        width = codes.shape[-1]
-        A.check(lib().tm_checkpoint8_unpack(_byref(ck.c()), _DT[out.dtype], codes.numel() // max(width, 1), width,
-                                            _p(out), _s(stream)), "tm_checkpoint8_unpack")
+    shape_ = codes.shape
+    if out is None:
+        out = codes.new_empty(shape_, dtype=ck.dtype)
+    dev = _lead("out", out)
+    width = shape_[-1]
+    st = A.load().tm_checkpoint8_unpack(ck.c("checkpoint", shape_, dev), _DT[out.dtype], codes.numel() // max(width, 1),
+                                        width, _arg("out", out, shape_, out.dtype, dev), _stream_of(None, dev))
+    if st:
+        A.check(st, "tm_checkpoint8_unpack")
     return out
 
 
-@dataclass
 class LayerNormSaved:
-    """What layer_norm's backward pass needs: each row's mean and 1 / std, and the checkpoint of
-    x + residual unless the caller keeps x and the residual themselves."""
-    mean: torch.Tensor
-    rstd: torch.Tensor
-    ckpt: Optional[Checkpoint8]
-    residual: bool                 # whether there was one
+    """What layer_norm's backward pass needs: each row's mean and 1 / std (stats [2, B, banks]), and the
+    checkpoint of x + residual unless the caller keeps x and the residual themselves."""
+    __slots__ = ("stats", "ckpt", "residual")
 
+    def __init__(self, stats: torch.Tensor, ckpt: Optional[Checkpoint8], residual: bool):
+        self.stats, self.ckpt, self.residual = stats, ckpt, residual
 
-def _norm_rows(name: str, x: torch.Tensor, layout: int, sh: A.tm_shape):
-    """(banks, width) of the rows that the norm sees in x, which is checked against sh."""
-    if x.shape[0] != sh.B or _DT.get(x.dtype) != sh.dtype:
-        raise ValueError(f"{name}: {tuple(x.shape)} {x.dtype} does not match the shape's batch {sh.B} and dtype")
-    if layout == A.TM_LAYOUT_MIXED:
-        if x.shape[1] != sh.T or x.shape[2] != sh.D:
-            raise ValueError(f"{name}: expected a token tensor [{sh.B}, {sh.T}, {sh.D}], got {tuple(x.shape)}")
-        return sh.H, sh.T * sh.D // sh.H
-    return x.shape[1], x.shape[2]
+    @property
+    def mean(self) -> torch.Tensor:
+        return self.stats[0]
+
+    @property
+    def rstd(self) -> torch.Tensor:
+        return self.stats[1]
 
 
 def layer_norm(x: torch.Tensor, residual: Optional[torch.Tensor], layout: int, sh: A.tm_shape,
@@ -959,24 +973,33 @@ def layer_norm(x: torch.Tensor, residual: Optional[torch.Tensor], layout: int, s
     """tm_layer_norm: (y, saved) with y = LN(x + residual) * gain + bias over rows.  x: rows
     [B, banks, width] or, with TM_LAYOUT_MIXED, a token tensor whose Mix rows are taken; residual and y
     are rows.  checkpoint8 keeps x + residual in 8 bits in `saved` for the backward pass."""
-    _lead("x", x, 3)
-    banks, width = _norm_rows("x", x, layout, sh)
-    rows, dt, dev = (sh.B, banks, width), x.dtype, x.device
-    _expect("residual", residual, rows, dt, dev)
-    _expect("gain", gain, (width,), dt, dev)
-    _expect("bias", bias, (width,), dt, dev)
-    with _on(stream):
-        if y is None:
-            y = torch.empty(rows, dtype=dt, device=dev)
-        else:
-            _expect("y", y, rows, dt, dev)
-        stats = torch.empty((2, (sh.B * banks + 3) // 4 * 4), dtype=torch.float32, device=dev)
-        mean, rstd = (stats[i, :sh.B * banks].view(sh.B, banks) for i in (0, 1))
-        ck = Checkpoint8.empty(rows, dt, dev) if checkpoint8 else None
-        w = A.tm_layer_norm_w(banks, width, _p(gain), _p(bias))
-        A.check(lib().tm_layer_norm(_p(x), _p(residual), layout, _byref(sh), _byref(w), _p(y), _p(mean), _p(rstd),
-                                    _byref(ck.c()) if ck is not None else None, _s(stream)), "tm_layer_norm")
-    return y, LayerNormSaved(mean, rstd, ck, residual is not None)
+    if stream is not None:
+        with _on(stream):
+            return layer_norm(x, residual, layout, sh, gain, bias, checkpoint8, y)
+    dev = _lead("x", x, 3)
+    dt, B = x.dtype, sh.B
+    if layout == A.TM_LAYOUT_MIXED:
+        banks, width = sh.H, sh.T * sh.D // max(sh.H, 1)
+        xshape, rows = (B, sh.T, sh.D), (B, banks, width)
+    else:
+        _, banks, width = x.shape
+        xshape = rows = (B, banks, width)
+    if _DT[dt] != sh.dtype:
+        raise ValueError(f"x: dtype {dt} does not match the shape's")
+    px = _arg("x", x, xshape, dt, dev)
+    if y is None:
+        y = torch.empty_like(x) if xshape == rows else x.new_empty(rows)
+    stats = x.new_empty((2, B, banks), dtype=torch.float32)
+    ck = Checkpoint8.like(x, rows) if checkpoint8 else None
+    mean = stats.data_ptr()
+    st = A.load().tm_layer_norm(
+        px, _arg("residual", residual, rows, dt, dev), layout, sh,
+        A.tm_layer_norm_w(banks, width, _arg("gain", gain, (width,), dt, dev), _arg("bias", bias, (width,), dt, dev)),
+        _arg("y", y, rows, dt, dev), mean, mean + 4 * B * banks, ck.c("checkpoint", rows, dev) if ck is not None else None,
+        _stream_of(None, dev))
+    if st:
+        A.check(st, "tm_layer_norm")
+    return y, LayerNormSaved(stats, ck, residual is not None)
 
 
 def layer_norm_backward(dy: torch.Tensor, saved: LayerNormSaved, layout: int, sh: A.tm_shape,
@@ -988,73 +1011,68 @@ def layer_norm_backward(dy: torch.Tensor, saved: LayerNormSaved, layout: int, sh
     dx itself and returned as such.  Mixed layout: dx is the gradient of the token tensor;
     residual_is_x adds the residual's gradient into it (one tensor X was both) and returns None for
     dresidual."""
-    _lead("dy", dy, 3)
-    dt, dev = dy.dtype, dy.device
+    if stream is not None:
+        with _on(stream):
+            return layer_norm_backward(dy, saved, layout, sh, gain, x, residual, residual_is_x, dx, workspace)
+    dev = _lead("dy", dy, 3)
+    dt, B = dy.dtype, sh.B
     mixed = layout == A.TM_LAYOUT_MIXED
-    banks, width = (sh.H, sh.T * sh.D // sh.H) if mixed else (dy.shape[1], dy.shape[2])
-    rows = (sh.B, banks, width)
-    _expect("dy", dy, rows, dt, dev)
+    if mixed:
+        banks, width = sh.H, sh.T * sh.D // max(sh.H, 1)
+        xshape, rows = (B, sh.T, sh.D), (B, banks, width)
+    else:
+        _, banks, width = dy.shape
+        xshape = rows = (B, banks, width)
     if _DT[dt] != sh.dtype:
         raise ValueError(f"dy: dtype {dt} does not match the shape's")
-    xshape = (sh.B, sh.T, sh.D) if mixed else rows
-    if saved.ckpt is None:
+    pdy = _arg("dy", dy, rows, dt, dev)
+    px = pres = ck = None
+    if saved.ckpt is not None:
+        ck = saved.ckpt.c("checkpoint", rows, dev)
+    else:
         if x is None or (saved.residual and residual is None):
             raise ValueError("layer_norm_backward needs x (and the residual) where no checkpoint was kept")
-        _expect("x", x, xshape, dt, dev)
-        _expect("residual", residual, rows, dt, dev)
-        if not saved.residual:
-            residual = None
-    else:
-        saved.ckpt.expect("checkpoint", rows, dev)
-        x = residual = None
-    _expect("gain", gain, (width,), dt, dev)
-    _expect("mean", saved.mean, rows[:2], torch.float32, dev)
-    _expect("rstd", saved.rstd, rows[:2], torch.float32, dev)
-    with _on(stream):
-        if dx is None:
-            dx = torch.empty(xshape, dtype=dt, device=dev)
-        else:
-            _expect("dx", dx, xshape, dt, dev)
-        dres = torch.empty(rows, dtype=dt, device=dev) if mixed and saved.residual and not residual_is_x else None
-        grads = {"dgain": torch.empty(width, dtype=dt, device=dev), "dbias": torch.empty(width, dtype=dt, device=dev)}
-        w = A.tm_layer_norm_w(banks, width, _p(gain), None)
-        n = lib().tm_layer_norm_backward_workspace_bytes(_byref(sh), layout, _byref(w))
-        ws = _ws(n, dev, workspace)
-        ck = saved.ckpt
-        A.check(lib().tm_layer_norm_backward(
-            _p(x), _p(residual), _byref(ck.c()) if ck is not None else None, _p(saved.mean), _p(saved.rstd), _p(dy),
-            layout, _byref(sh), _byref(w), 1 if residual_is_x and mixed else 0, _p(dx), _p(dres),
-            _byref(A.tm_layer_norm_grads(_p(grads["dgain"]), _p(grads["dbias"]))), _p(ws), ws.numel(), _s(stream)),
-            "tm_layer_norm_backward")
+        px = _arg("x", x, xshape, dt, dev)
+        if saved.residual:
+            pres = _arg("residual", residual, rows, dt, dev)
+    mean = _arg("saved statistics", saved.stats, (2, B, banks), torch.float32, dev)
+    if dx is None:
+        dx = torch.empty_like(dy) if xshape == rows else dy.new_empty(xshape)
+    self_ = residual_is_x and mixed
+    dres = dy.new_empty(rows) if mixed and saved.residual and not self_ else None
+    dgain, dbias = dy.new_empty(width), dy.new_empty(width)
+    lib_ = A.load()
+    w = A.tm_layer_norm_w(banks, width, _arg("gain", gain, (width,), dt, dev), None)
+    n = lib_.tm_layer_norm_backward_workspace_bytes(sh, layout, w)
+    ws = _ws(n, dy.device, workspace)
+    st = lib_.tm_layer_norm_backward(
+        px, pres, ck, mean, mean + 4 * B * banks, pdy, layout, sh, w, 1 if self_ else 0, _arg("dx", dx, xshape, dt, dev),
+        None if dres is None else dres.data_ptr(), A.tm_layer_norm_grads(dgain.data_ptr(), dbias.data_ptr()), _p(ws),
+        ws.numel(), _stream_of(None, dev))
+    if st:
+        A.check(st, "tm_layer_norm_backward")
     if not mixed and saved.residual:
         dres = dx
-    return dx, dres, grads
+    return dx, dres, {"dgain": dgain, "dbias": dbias}
 
 
-@dataclass
 class Linear:
     """A per-token linear layer: w [banks, out, width], bias [banks, out] or None, and an activation
     (none, relu, gelu, silu)."""
-    w: torch.Tensor
-    bias: Optional[torch.Tensor] = None
-    act: str = "none"
+    __slots__ = ("w", "bias", "act")
 
-    def c(self) -> A.tm_linear_w:
-        banks, out, width = self.w.shape
-        return A.tm_linear_w(banks, width, out, _ACTS[self.act], _p(self.w), _p(self.bias))
+    def __init__(self, w: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none"):
+        if act not in _ACTS:
+            raise ValueError(f"activation {act!r}: one of {sorted(_ACTS)}")
+        if w.dim() != 3:
+            raise ValueError(f"w: expected [banks, out, width], got {tuple(w.shape)}")
+        self.w, self.bias, self.act = w, bias, act
 
-
-def _linear_check(x: torch.Tensor, lin: Linear):
-    _lead("x", x, 3)
-    if lin.act not in _ACTS:
-        raise ValueError(f"activation {lin.act!r}: one of {sorted(_ACTS)}")
-    if lin.w.dim() != 3:
-        raise ValueError(f"w: expected [banks, out, width], got {tuple(lin.w.shape)}")
-    B, banks, width = x.shape
-    out = lin.w.shape[1]
-    _expect("w", lin.w, (banks, out, width), x.dtype, x.device)
-    _expect("bias", lin.bias, (banks, out), x.dtype, x.device)
-    return A.tm_shape(B, banks, width, 1, _DT[x.dtype], 0.0), (B, banks, out)
+    def c(self, banks: int, width: int, dtype, dev: int) -> A.tm_linear_w:
+        """The C descriptor, the tensors checked against the input rows'."""
+        out = self.w.shape[1]
+        return A.tm_linear_w(banks, width, out, _ACTS[self.act], _arg("w", self.w, (banks, out, width), dtype, dev),
+                             _arg("bias", self.bias, (banks, out), dtype, dev))
 
 
 def pertoken_linear(x: torch.Tensor, lin: Linear, residual: Optional[torch.Tensor] = None,
@@ -1062,24 +1080,31 @@ def pertoken_linear(x: torch.Tensor, lin: Linear, residual: Optional[torch.Tenso
     """tm_pertoken_linear: y = act(x w^T + bias) + residual per bank; x [B, banks, width], y and residual
     [B, banks, out].  save "full" or "ckpt8": returns (y, saved), saved the pre-activation in the storage
     dtype or as a Checkpoint8 (None without an activation, whose backward pass needs neither)."""
-    sh, rows = _linear_check(x, lin)
-    dt, dev = x.dtype, x.device
-    if save not in (None, "full", "ckpt8"):
-        raise ValueError(f"save {save!r}: None, 'full' or 'ckpt8'")
-    _expect("residual", residual, rows, dt, dev)
-    with _on(stream):
-        if y is None:
-            y = torch.empty(rows, dtype=dt, device=dev)
-        else:
-            _expect("y", y, rows, dt, dev)
-        z = ck = None
+    if stream is not None:
+        with _on(stream):
+            return pertoken_linear(x, lin, residual, save, y)
+    dev = _lead("x", x, 3)
+    dt = x.dtype
+    B, banks, width = xshape = x.shape
+    rows = (B, banks, lin.w.shape[1])
+    c = lin.c(banks, width, dt, dev)
+    if y is None:
+        y = x.new_empty(rows)
+    z = ck = None
+    if save is not None:
+        if save not in ("full", "ckpt8"):
+            raise ValueError(f"save {save!r}: None, 'full' or 'ckpt8'")
         if lin.act != "none":
             if save == "full":
-                z = torch.empty(rows, dtype=dt, device=dev)
-            elif save == "ckpt8":
-                ck = Checkpoint8.empty(rows, dt, dev)
-        A.check(lib().tm_pertoken_linear(_p(x), _p(residual), _byref(sh), _byref(lin.c()), _p(y), _p(z),
-                                         _byref(ck.c()) if ck is not None else None, _s(stream)), "tm_pertoken_linear")
+                z = torch.empty_like(y)
+            else:
+                ck = Checkpoint8.like(x, rows)
+    st = A.load().tm_pertoken_linear(
+        _arg("x", x, xshape, dt, dev), _arg("residual", residual, rows, dt, dev),
+        A.tm_shape(B, banks, width, 1, _DT[dt], 0.0), c, _arg("y", y, rows, dt, dev),
+        None if z is None else z.data_ptr(), None if ck is None else ck.c("checkpoint", rows, dev), _stream_of(None, dev))
+    if st:
+        A.check(st, "tm_pertoken_linear")
     return y if save is None else (y, ck if z is None else z)
 
 
@@ -1088,35 +1113,38 @@ def pertoken_linear_backward(x: torch.Tensor, dy: torch.Tensor, lin: Linear, sav
                              workspace=None, stream=None):
     """tm_pertoken_linear_backward: (dx, {dw, db}) for the gradient dy of y (db only with a bias); saved:
     what pertoken_linear kept.  dx = dz w + dx_add.  The residual's gradient is dy."""
-    sh, rows = _linear_check(x, lin)
-    dt, dev = x.dtype, x.device
-    _expect("dy", dy, rows, dt, dev)
-    _expect("dx_add", dx_add, x.shape, dt, dev)
+    if stream is not None:
+        with _on(stream):
+            return pertoken_linear_backward(x, dy, lin, saved, dx_add, dx, workspace)
+    dev = _lead("x", x, 3)
+    dt = x.dtype
+    B, banks, width = xshape = x.shape
+    rows = (B, banks, lin.w.shape[1])
+    c = lin.c(banks, width, dt, dev)
+    sh = A.tm_shape(B, banks, width, 1, _DT[dt], 0.0)
     z = ck = None
     if lin.act != "none":
-        if isinstance(saved, Checkpoint8):
-            ck = saved
-            ck.expect("saved", rows, dev)
-        elif saved is not None:
-            z = saved
-            _expect("saved", z, rows, dt, dev)
-        else:
+        if saved is None:
             raise ValueError("pertoken_linear_backward of an activation needs what the forward kept (save=...)")
-    with _on(stream):
-        if dx is None:
-            dx = torch.empty(x.shape, dtype=dt, device=dev)
+        if isinstance(saved, Checkpoint8):
+            ck = saved.c("saved", rows, dev)
         else:
-            _expect("dx", dx, x.shape, dt, dev)
-        grads = {"dw": torch.empty(lin.w.shape, dtype=dt, device=dev)}
-        if lin.bias is not None:
-            grads["db"] = torch.empty(lin.bias.shape, dtype=dt, device=dev)
-        c = lin.c()
-        n = lib().tm_pertoken_linear_backward_workspace_bytes(_byref(sh), _byref(c))
-        ws = _ws(n, dev, workspace)
-        A.check(lib().tm_pertoken_linear_backward(
-            _p(x), _p(dy), _p(z), _byref(ck.c()) if ck is not None else None, _p(dx_add), _byref(sh), _byref(c), _p(dx),
-            _byref(A.tm_linear_grads(_p(grads["dw"]), _p(grads.get("db")))), _p(ws), ws.numel(), _s(stream)),
-            "tm_pertoken_linear_backward")
+            z = _arg("saved", saved, rows, dt, dev)
+    if dx is None:
+        dx = torch.empty_like(x)
+    grads = {"dw": torch.empty_like(lin.w)}
+    if lin.bias is not None:
+        grads["db"] = torch.empty_like(lin.bias)
+    lib_ = A.load()
+    n = lib_.tm_pertoken_linear_backward_workspace_bytes(sh, c)
+    ws = _ws(n, x.device, workspace)
+    st = lib_.tm_pertoken_linear_backward(
+        _arg("x", x, xshape, dt, dev), _arg("dy", dy, rows, dt, dev), z, ck, _arg("dx_add", dx_add, xshape, dt, dev), sh, c,
+        _arg("dx", dx, xshape, dt, dev),
+        A.tm_linear_grads(grads["dw"].data_ptr(), grads["db"].data_ptr() if "db" in grads else None), _p(ws), ws.numel(),
+        _stream_of(None, dev))
+    if st:
+        A.check(st, "tm_pertoken_linear_backward")
     return dx, grads
 
 

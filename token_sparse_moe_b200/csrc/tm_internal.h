@@ -144,16 +144,20 @@ cudaError_t launch_ckpt8(bool pack, int dtype, void* x, void* codes, void* exps,
 int norm_max_width();
 bool ln_self_supported(int H, int W);
 size_t ln_part_floats(long long nrows, int W, int sms);
-cudaError_t launch_ln_fwd(int dtype, const NormParams& p, cudaStream_t st);
+cudaError_t launch_ln_fwd(int dtype, const NormParams& p, int sms, cudaStream_t st);
 cudaError_t launch_ln_bwd(int dtype, const NormParams& p, bool self, void* dgain, void* dbias, int sms,
                           cudaStream_t st);
 cudaError_t launch_linear_simt(const SimtLin& p, cudaStream_t st);
-cudaError_t launch_linear_fwd(int bn, int act, int save, const CUtensorMap& a, const CUtensorMap& b,
-                              const CUtensorMap& o, const CUtensorMap& z, const LinParams& p, int sms, cudaStream_t st);
-cudaError_t launch_linear_dx(int bn, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
-                             const LinParams& p, int sms, cudaStream_t st);
-cudaError_t launch_linear_dw(int bn, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
-                             const LinParams& p, int sms, cudaStream_t st);
+// Tensor maps of one contraction: operands, D (or fp32 partial sums), addend, z or codes (the last two
+// any valid map where they are not used)
+struct LinMaps {
+    CUtensorMap a, b, o, r, z;
+};
+// pair: CTA pairs (tiles of 256 x 256), else 128 x 128
+cudaError_t launch_linear_fwd(bool pair, int act, int save, const LinMaps& m, const LinParams& p, int sms,
+                              cudaStream_t st);
+cudaError_t launch_linear_dx(bool pair, const LinMaps& m, const LinParams& p, int sms, cudaStream_t st);
+cudaError_t launch_linear_dw(bool pair, const LinMaps& m, const LinParams& p, int sms, cudaStream_t st);
 // out[i] = sum over r < R of part[r][i]
 cudaError_t launch_sum_parts(int dtype, const float* part, int R, long long n, void* out, cudaStream_t st);
 int act_bwd_chunks(int dtype, int B, long long cols, int N, int sms);

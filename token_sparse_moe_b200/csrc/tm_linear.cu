@@ -1,6 +1,8 @@
 // tm_linear.cu -- the per-token linear layer beside its tensor-core contractions (tm_linear.cuh): the
 // activation's derivative with the bias gradient's column sums, the sums of partial results, the fp32
 // form of the contractions on CUDA cores, and the launchers.
+#include <string.h>
+
 #include <atomic>
 
 #include "tm_linear.cuh"
@@ -219,11 +221,10 @@ cudaError_t launch_linear_simt(const SimtLin& p, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <int BN, bool A_MN, bool B_MN, int ACT, int SAVE, bool F32OUT>
-static cudaError_t launch_linear_one(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
-                                     const CUtensorMap& z, const LinParams& p, int sms, cudaStream_t st) {
-    using C = LinCfg<BN, SAVE>;
-    auto kern = linear_gemm_kernel<BN, A_MN, B_MN, ACT, SAVE, F32OUT>;
+template <int BN, bool PAIR, bool A_MN, bool B_MN, int ACT, int SAVE, bool F32OUT>
+static cudaError_t launch_linear_one(const LinMaps& m, const LinParams& p, int sms, cudaStream_t st) {
+    using C = LinCfg<BN, PAIR, SAVE>;
+    auto kern = linear_gemm_kernel<BN, PAIR, A_MN, B_MN, ACT, SAVE, F32OUT>;
     static std::atomic<bool> configured[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -233,48 +234,52 @@ static cudaError_t launch_linear_one(const CUtensorMap& a, const CUtensorMap& b,
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
     }
-    const long long tiles = (long long)p.groups * p.splits * p.mt * p.nt;
     ProfileScope ps_(A_MN ? "linear_dw" : B_MN ? "linear_dx" : "linear", st);
-    kern<<<(int)(tiles < sms ? tiles : sms), C::NTHREADS, C::SMEM_BYTES, st>>>(a, b, o, z, p);
-    return cudaGetLastError();
+    if (!PAIR) {
+        kern<<<p.ntile < sms ? p.ntile : sms, C::NTHREADS, C::SMEM_BYTES, st>>>(m.a, m.b, m.o, m.r, m.z, p);
+        return cudaGetLastError();
+    }
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3((unsigned)(2 * (p.ntile < sms / 2 ? p.ntile : sms / 2)), 1, 1);
+    cfg.blockDim = dim3(C::NTHREADS, 1, 1);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, m.a, m.b, m.o, m.r, m.z, p);
 }
 
-template <int BN>
-static cudaError_t launch_linear_fwd_bn(int act, int save, const CUtensorMap& a, const CUtensorMap& b,
-                                        const CUtensorMap& o, const CUtensorMap& z, const LinParams& p, int sms,
-                                        cudaStream_t st) {
-    if (act == LIN_NONE)
-        return launch_linear_one<BN, false, false, LIN_NONE, LIN_KEEP_NOTHING, false>(a, b, o, z, p, sms, st);
+// The two shapes of tile: pairs of 256 x 256, single CTAs of 128 x 128.
+template <bool A_MN, bool B_MN, int ACT, int SAVE, bool F32OUT>
+static cudaError_t launch_linear_shape(bool pair, const LinMaps& m, const LinParams& p, int sms, cudaStream_t st) {
+    if (pair) return launch_linear_one<256, true, A_MN, B_MN, ACT, SAVE, F32OUT>(m, p, sms, st);
+    return launch_linear_one<128, false, A_MN, B_MN, ACT, SAVE, F32OUT>(m, p, sms, st);
+}
+
+cudaError_t launch_linear_fwd(bool pair, int act, int save, const LinMaps& m, const LinParams& p, int sms,
+                              cudaStream_t st) {
+    if (act == LIN_NONE) return launch_linear_shape<false, false, LIN_NONE, LIN_KEEP_NOTHING, false>(pair, m, p, sms, st);
 #define X(ACT_, SAVE_) \
-    if (act == ACT_ && save == SAVE_) \
-        return launch_linear_one<BN, false, false, ACT_, SAVE_, false>(a, b, o, z, p, sms, st);
+    if (act == ACT_ && save == SAVE_) return launch_linear_shape<false, false, ACT_, SAVE_, false>(pair, m, p, sms, st);
     X(LIN_RELU, LIN_KEEP_NOTHING) X(LIN_RELU, LIN_KEEP_FULL) X(LIN_RELU, LIN_KEEP_CK8)
     X(LIN_GELU, LIN_KEEP_NOTHING) X(LIN_GELU, LIN_KEEP_FULL) X(LIN_GELU, LIN_KEEP_CK8)
     X(LIN_SILU, LIN_KEEP_NOTHING) X(LIN_SILU, LIN_KEEP_FULL) X(LIN_SILU, LIN_KEEP_CK8)
 #undef X
     return cudaErrorInvalidValue;
 }
-
-// bn: 256 or 128 columns a tile
-cudaError_t launch_linear_fwd(int bn, int act, int save, const CUtensorMap& a, const CUtensorMap& b,
-                              const CUtensorMap& o, const CUtensorMap& z, const LinParams& p, int sms,
-                              cudaStream_t st) {
-    return bn == 256 ? launch_linear_fwd_bn<256>(act, save, a, b, o, z, p, sms, st)
-                     : launch_linear_fwd_bn<128>(act, save, a, b, o, z, p, sms, st);
+cudaError_t launch_linear_dx(bool pair, const LinMaps& m, const LinParams& p, int sms, cudaStream_t st) {
+    return launch_linear_shape<false, true, LIN_NONE, LIN_KEEP_NOTHING, false>(pair, m, p, sms, st);
 }
-cudaError_t launch_linear_dx(int bn, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
-                             const LinParams& p, int sms, cudaStream_t st) {
-    return bn == 256 ? launch_linear_one<256, false, true, LIN_NONE, LIN_KEEP_NOTHING, false>(a, b, o, o, p, sms, st)
-                     : launch_linear_one<128, false, true, LIN_NONE, LIN_KEEP_NOTHING, false>(a, b, o, o, p, sms, st);
-}
-// p.splits > 1: fp32 partial sums through o
-cudaError_t launch_linear_dw(int bn, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
-                             const LinParams& p, int sms, cudaStream_t st) {
-    if (p.splits > 1)
-        return bn == 256 ? launch_linear_one<256, true, true, LIN_NONE, LIN_KEEP_NOTHING, true>(a, b, o, o, p, sms, st)
-                         : launch_linear_one<128, true, true, LIN_NONE, LIN_KEEP_NOTHING, true>(a, b, o, o, p, sms, st);
-    return bn == 256 ? launch_linear_one<256, true, true, LIN_NONE, LIN_KEEP_NOTHING, false>(a, b, o, o, p, sms, st)
-                     : launch_linear_one<128, true, true, LIN_NONE, LIN_KEEP_NOTHING, false>(a, b, o, o, p, sms, st);
+// more than one split: fp32 partial sums
+cudaError_t launch_linear_dw(bool pair, const LinMaps& m, const LinParams& p, int sms, cudaStream_t st) {
+    if (p.splits.d > 1) return launch_linear_shape<true, true, LIN_NONE, LIN_KEEP_NOTHING, true>(pair, m, p, sms, st);
+    return launch_linear_shape<true, true, LIN_NONE, LIN_KEEP_NOTHING, false>(pair, m, p, sms, st);
 }
 
 cudaError_t launch_sum_parts(int dtype, const float* part, int R, long long n, void* out, cudaStream_t st) {

@@ -7,16 +7,19 @@
 // contraction index is not the contiguous one (W in dX, both in dW) is loaded by TMA as it lies --
 // boxes of 64 contiguous elements by 64 contraction rows -- and multiplied as an MN-major operand.
 //
-// Tile: 128 rows x BN columns, contraction in slabs of 64, 128-byte swizzle; edges in any direction
-// are the tensor maps' business (loads past an extent give zeros, stores past it are dropped), so
-// sizes need only be multiples of 8 (16-byte strides).  Persistent CTAs, one per SM: warp 0 issues the
-// TMA loads, warp 1 the MMAs, warps 2-9 are the epilogue (two per TMEM lane quarter, each half of the
-// columns).  Two accumulators in TMEM let the epilogue of a tile overlap the MMAs of the next.
+// Tile: 128 rows x BN columns, contraction in slabs of 64, 128-byte swizzle; edges in any direction are
+// zeros from the tensor maps (loads past an extent) and predicates (stores), so sizes need only be
+// multiples of 8 (16-byte strides).  Persistent CTAs, one per SM: warp 0 issues the TMA loads, warp 1
+// the MMAs, warps 2-9 are the epilogue (two per TMEM lane quarter, each half of the columns).  Two
+// accumulators in TMEM let the epilogue of a tile overlap the MMAs of the next.
 //
-// Epilogue: 32 columns at a time.  Eight warps share the activation: per 128 x 256 tile it costs one
-// exponential per element (2048 cycles of the SM's 16 per cycle), which a contraction of 512 or more
-// covers.  The output leaves through a 2 KB box per warp (32 rows x 64 bytes, 64-byte swizzle), two of
-// them in turn so that a bulk store reads one while the other is filled.
+// Pair mode (PAIR): a cluster of two CTAs on 256 rows, each holding its 128 A rows and half of the B
+// rows, one tcgen05.mma.cta_group::2 for both.  A tile's operands are then 32 KB a slab and SM instead
+// of 48: the plain form is bound by what the L2 delivers to the SMs.
+//
+// Epilogue: 32 columns at a time, the next 32 on their way from TMEM.  Eight warps share the activation:
+// per 128 x 256 tile it costs one exponential per element (2048 cycles of the SM's 16 per cycle), which
+// a contraction of depth 256 (2048 tensor cycles) covers.
 #pragma once
 #include "tm_ckpt8.cuh"
 #include "tm_gemm.cuh"
@@ -27,31 +30,50 @@ enum LinAct : int { LIN_NONE = 0, LIN_RELU = 1, LIN_GELU = 2, LIN_SILU = 3 };
 // what the forward keeps of the pre-activation
 enum LinSave : int { LIN_KEEP_NOTHING = 0, LIN_KEEP_FULL = 1, LIN_KEEP_CK8 = 2 };
 
+// Quotients by a fixed divisor d of 0 <= t < 2^31: (umulhi(m, t) + t) >> l, l = ceil(log2 d),
+// m = floor(2^32 (2^l - d) / d) + 1 (division by an invariant integer through multiplication).
+struct FastDiv {
+    uint32_t d, m, l;
+    __device__ __forceinline__ int div(int t) const { return (int)((__umulhi(m, (uint32_t)t) + (uint32_t)t) >> l); }
+};
+inline FastDiv fast_div(uint32_t d) {
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    return FastDiv{d, (uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1), l};
+}
+
 struct LinParams {
     int groups;                // banks
     int rows, cols, depth;     // extents of D and of the contraction, per bank
-    int mt, nt;                // tiles
-    int splits, split_slabs;   // the contraction in `splits` runs of at most split_slabs slabs of 64
+    FastDiv mt, nt, splits;    // tiles: rows (of 128, pair mode 256) and columns; runs of the contraction
+    int ntile;                 // groups * splits * mt * nt
+    int split_slabs;           // slabs of 64 of a run, at most
     const __nv_bfloat16* bias;   // [groups, cols] or NULL
-    const __nv_bfloat16* add;    // residual / dx_add in D's layout or NULL
-    size_t add_row, add_group;   // its strides: rows, groups
-    int8_t* codes;             // LIN_KEEP_CK8: [rows * groups, cols]
+    int add;                   // residual / dx_add in D's layout (its map: tmR)
+    int8_t* codes;             // LIN_KEEP_CK8: [rows * groups, cols], and
     int8_t* exps;              //               [rows * groups, nblk]
     int nblk;
 };
 
-template <int BN, int SAVE>
+template <int BN, bool PAIR, int SAVE>
 struct LinCfg {
-    static constexpr int BM = 128;
-    static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
+    static constexpr int BM = 128;                  // rows of D per CTA (a pair: 256)
+    static constexpr int BC = PAIR ? BN / 2 : BN;   // B rows that this CTA loads
+    static constexpr int A_BYTES = BM * 128, B_BYTES = BC * 128;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int EPI_WARPS = 8;
+    static constexpr int EPI_WARPS = BN / 16;       // 4 lane quarters x BN / 64 column blocks
     static constexpr int NTHREADS = 32 * (2 + EPI_WARPS);
-    static constexpr int STG_BYTES = EPI_WARPS * 4096;
-    static constexpr int STAGES = (232448 - 1024 - 256 - STG_BYTES) / STAGE_BYTES;
-    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STG_BYTES + 1024 + 256;
+    // an epilogue warp's boxes: 32 rows x 64 bf16 of D, beside it the same of z or the codes
+    static constexpr int BOX_BYTES = 4096 + (SAVE == LIN_KEEP_FULL ? 4096 : SAVE == LIN_KEEP_CK8 ? 2048 : 0);
+    static constexpr int STG_BYTES = EPI_WARPS * BOX_BYTES;
+    static constexpr int BIAS_BYTES = 2 * BN * 4;   // the tile's bias in fp32, tiles in turn
+    static constexpr int BAR_BYTES = 320;
+    static constexpr int STAGES_ = (232448 - BAR_BYTES - STG_BYTES - BIAS_BYTES) / STAGE_BYTES;
+    static constexpr int STAGES = STAGES_ > 6 ? 6 : STAGES_;
+    static constexpr int OFF_STG = STAGES * STAGE_BYTES, OFF_BIAS = OFF_STG + STG_BYTES, OFF_BAR = OFF_BIAS + BIAS_BYTES;
+    static constexpr int SMEM_BYTES = OFF_BAR + BAR_BYTES;
     static constexpr int TMEM_COLS = 2 * BN;
-    static_assert(SMEM_BYTES <= 232448 && STAGES >= 3 && (16 * STAGES + 48) <= 256, "shared memory budget");
+    static_assert(SMEM_BYTES <= 232448 && STAGES >= 3 && 16 * STAGES + 48 + 8 * EPI_WARPS <= BAR_BYTES, "shared memory budget");
     static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "tensor memory");
 };
 
@@ -68,6 +90,13 @@ __device__ __forceinline__ uint64_t umma_sdesc_mn128(uint32_t saddr) {
     return d;
 }
 constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
+
+// Arrive on the leader's accumulator-free barrier.  Nothing in memory is handed over with it -- the
+// tensor-memory loads are complete and fenced -- so release at CTA scope does; at cluster scope it waited
+// 2000 to 4000 cycles a tile for the thread's outstanding global writes.
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 
 __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
     float r;
@@ -120,22 +149,33 @@ __device__ __forceinline__ float2 lin_act2(float2 z) {
     return z;
 }
 
-template <int BN, bool A_MN, bool B_MN, int ACT, int SAVE, bool F32OUT>
-__global__ void __launch_bounds__(LinCfg<BN, SAVE>::NTHREADS, 1)
+// D's rows are matrix rows, [bank][rows][cols], when A is MN-major (dW), else samples, [rows][bank][cols].
+// Maps: tmO D (or the fp32 partial sums), tmR the addend, tmZ z or the codes, all in boxes of 32 rows.
+template <int BN, bool PAIR, bool A_MN, bool B_MN, int ACT, int SAVE, bool F32OUT>
+__global__ void __launch_bounds__(LinCfg<BN, PAIR, SAVE>::NTHREADS, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                       const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmZ,
-                       const LinParams p) {
-    using C = LinCfg<BN, SAVE>;
+                       const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmR,
+                       const __grid_constant__ CUtensorMap tmZ, const LinParams p) {
+    using C = LinCfg<BN, PAIR, SAVE>;
     constexpr int STAGES = C::STAGES;
-    const int ntile = p.groups * p.splits * p.mt * p.nt;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE_BYTES + C::STG_BYTES);
+    constexpr bool OUT_MAT = A_MN;
+    const int rank = PAIR ? (int)cluster_ctarank() : 0;
+    const bool leader = rank == 0;
+    const int cid = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+    const int ncid = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+    extern __shared__ __align__(1024) uint8_t lin_smem[];
+    uint8_t* smem = lin_smem;
+    if (smem_u32(smem) & 1023u) {            // the swizzled tiles need it; never so (checked, not assumed)
+        if (threadIdx.x == 0) record_error(ERR_BOUNDS, 0x806);
+        return;                              // the same in both CTAs of a pair
+    }
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t* empty = full + STAGES;
     uint64_t* acc_full = empty + STAGES;
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* drain = acc_empty + 2;
-    uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* add_full = drain + 1;          // [EPI_WARPS] the addend of a warp's box has landed
+    uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(add_full + C::EPI_WARPS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_smem + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -146,13 +186,15 @@ __global__ void __launch_bounds__(LinCfg<BN, SAVE>::NTHREADS, 1)
     // columns innermost, then row blocks: CTAs side by side share a row block's A tile and the bank's B
     auto decode = [&](int t) -> Tile {
         Tile r;
-        r.n = t % p.nt;
-        t /= p.nt;
-        r.m = t % p.mt;
-        t /= p.mt;
-        r.s = t % p.splits;
-        r.g = t / p.splits;
+        int u = p.nt.div(t);
+        r.n = t - u * p.nt.d;
+        t = u;
+        u = p.mt.div(t);
+        r.m = t - u * p.mt.d;
+        r.g = p.splits.div(u);
+        r.s = u - r.g * p.splits.d;
         r.slabs = min(p.split_slabs, slabs_all - r.s * p.split_slabs);
+        if (PAIR) r.m = 2 * r.m + rank;      // this CTA's 128 rows (past the extent: loaded as zeros, not stored)
         return r;
     };
 
@@ -163,18 +205,25 @@ __global__ void __launch_bounds__(LinCfg<BN, SAVE>::NTHREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], C::EPI_WARPS);
+            mbar_init(&acc_empty[b], C::EPI_WARPS * (PAIR ? 2 : 1));
         }
         mbar_init(drain, 1);
+        for (int w = 0; w < C::EPI_WARPS; ++w) mbar_init(&add_full[w], 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc(tmem_base_smem, C::TMEM_COLS);
-        tmem_relinquish();
+        if (PAIR) {
+            tmem_alloc_pair(tmem_base_smem, C::TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_base_smem, C::TMEM_COLS);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
-    __syncthreads();
+    if (PAIR) cluster_sync_all();            // both CTAs' barriers exist before any remote use
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_base_smem;
 
@@ -186,202 +235,209 @@ __global__ void __launch_bounds__(LinCfg<BN, SAVE>::NTHREADS, 1)
             int s = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < ntile && ok; t += gridDim.x) {
+            for (int t = cid; t < p.ntile && ok; t += ncid) {
                 const Tile ti = decode(t);
+                // pair mode: each CTA loads half of the tile's B rows
+                const int n0 = ti.n * BN + (PAIR ? rank * C::BC : 0);
                 for (int kb = 0; kb < ti.slabs; ++kb) {
                     if (!wait_or_abort(&empty[s], ph ^ 1, abort_flag, 0x800)) { ok = false; break; }
                     uint8_t* sa = smem + s * C::STAGE_BYTES;
                     uint8_t* sb = sa + C::A_BYTES;
                     const int k0 = (ti.s * p.split_slabs + kb) * 64;
-                    mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
+                    if (leader) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * C::STAGE_BYTES);
+                    const uint32_t lbar = PAIR ? mapa_shared(smem_u32(&full[s]), 0) : 0u;   // the leader's barrier
+                    auto ld3 = [&](void* dst, const CUtensorMap* m, int c0, int c1, int c2) {
+                        if (PAIR) tma_load_3d_pair(dst, m, lbar, c0, c1, c2);
+                        else tma_load_3d(dst, m, &full[s], c0, c1, c2);
+                    };
                     if constexpr (A_MN) {        // [depth rows][bank][rows of D]: two blocks of 64
-                        tma_load_3d(sa, &tmA, &full[s], ti.m * 128, ti.g, k0);
-                        tma_load_3d(sa + 8192, &tmA, &full[s], ti.m * 128 + 64, ti.g, k0);
+                        ld3(sa, &tmA, ti.m * 128, ti.g, k0);
+                        ld3(sa + 8192, &tmA, ti.m * 128 + 64, ti.g, k0);
                     } else {                     // [rows of D][bank][depth]
-                        tma_load_3d(sa, &tmA, &full[s], k0, ti.g, ti.m * 128);
+                        ld3(sa, &tmA, k0, ti.g, ti.m * 128);
                     }
                     if constexpr (B_MN) {
 #pragma unroll
-                        for (int i = 0; i < BN / 64; ++i) {
+                        for (int i = 0; i < C::BC / 64; ++i) {
                             if constexpr (A_MN)  // x: [depth rows][bank][columns of D]
-                                tma_load_3d(sb + i * 8192, &tmB, &full[s], ti.n * BN + i * 64, ti.g, k0);
+                                ld3(sb + i * 8192, &tmB, n0 + i * 64, ti.g, k0);
                             else                 // W: [bank][depth rows][columns of D]
-                                tma_load_3d(sb + i * 8192, &tmB, &full[s], ti.n * BN + i * 64, k0, ti.g);
+                                ld3(sb + i * 8192, &tmB, n0 + i * 64, k0, ti.g);
                         }
                     } else {                     // W: [bank][columns of D][depth]
-                        tma_load_3d(sb, &tmB, &full[s], k0, ti.n * BN, ti.g);
+                        ld3(sb, &tmB, k0, n0, ti.g);
                     }
                     if (issued < STAGES) ++issued;
                     if (++s == STAGES) { s = 0; ph ^= 1; }
                 }
             }
-            // given up: the loads in flight land (a bounded wait each) before the block may end
             if (!ok || *abort_flag) {
-                for (int i = 0; i < issued; ++i) {
-                    if (s == 0) { s = STAGES; ph ^= 1; }
-                    --s;
-                    mbar_wait(&full[s], ph, 0x804);
+                // given up: the loads in flight land before the block may end -- a bounded wait for each,
+                // or in a pair, whose loads the leader's barriers count, a millisecond
+                if (PAIR) {
+                    for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000;) {}
+                } else {
+                    for (int i = 0; i < issued; ++i) {
+                        if (s == 0) { s = STAGES; ph ^= 1; }
+                        --s;
+                        mbar_wait(&full[s], ph, 0x804);
+                    }
                 }
             }
         }
     } else if (warp == 1) {
-        // ---------------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t idesc = umma_idesc_bf16(128, BN) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
+        // ---------------------------------------------------------------- MMA issuer (pair: the leader's)
+        if (lane == 0 && leader) {
+            constexpr uint32_t idesc =
+                umma_idesc_bf16(PAIR ? 256 : 128, BN) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
+            auto commit = [&](uint64_t* b) {
+                if (PAIR) umma_commit_both(b);
+                else umma_commit(b);
+            };
+            const uint32_t sbase = smem_u32(smem);
             int s = 0, lt = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < ntile && ok; t += gridDim.x, ++lt) {
-                const Tile ti = decode(t);
+            for (int t = cid; t < p.ntile && ok; t += ncid, ++lt) {
+                const int slabs = decode(t).slabs;
                 const int buf = lt & 1;
-                if (!wait_or_abort(&acc_empty[buf], ((lt >> 1) & 1) ^ 1, abort_flag, 0x801)) break;
+                // the peer's warps arrive here too
+                if (!(PAIR ? wait_or_abort_cl(&acc_empty[buf], ((lt >> 1) & 1) ^ 1, abort_flag, 0x801)
+                           : wait_or_abort(&acc_empty[buf], ((lt >> 1) & 1) ^ 1, abort_flag, 0x801)))
+                    break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + buf * BN;
-                for (int kb = 0; kb < ti.slabs; ++kb) {
+                for (int kb = 0; kb < slabs; ++kb) {
                     if (!wait_or_abort(&full[s], ph, abort_flag, 0x802)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + s * C::STAGE_BYTES);
-                    const uint32_t sb = sa + C::A_BYTES;
+                    const uint32_t sa = sbase + s * C::STAGE_BYTES, sb = sa + C::A_BYTES;
                     const uint64_t ad = A_MN ? umma_sdesc_mn128(sa) : umma_sdesc_sw128(sa);
                     const uint64_t bd = B_MN ? umma_sdesc_mn128(sb) : umma_sdesc_sw128(sb);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16(d, ad + (A_MN ? 128 : 2) * kk, bd + (B_MN ? 128 : 2) * kk, idesc, (kb | kk) != 0);
-                    umma_commit(&empty[s]);
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint64_t ak = ad + (A_MN ? 128 : 2) * kk, bk = bd + (B_MN ? 128 : 2) * kk;
+                        if (PAIR) umma_bf16_pair(d, ak, bk, idesc, (kb | kk) != 0);
+                        else umma_bf16(d, ak, bk, idesc, (kb | kk) != 0);
+                    }
+                    commit(&empty[s]);
                     if (++s == STAGES) { s = 0; ph ^= 1; }
                 }
                 if (!ok) break;
-                umma_commit(&acc_full[buf]);
+                commit(&acc_full[buf]);
             }
             // every MMA issued is complete before the tensor memory is released
-            umma_commit(drain);
+            if (PAIR) umma_commit_pair(mapa_shared(smem_u32(drain), 0));
+            else umma_commit(drain);
             mbar_wait(drain, 0, 0x805);
         }
     } else {
         // ---------------------------------------------------------------- epilogue
-        const int q = warp & 3, half = (warp - 2) >> 2;
-        constexpr int HC = BN / 2;                      // columns of this warp
-        uint8_t* stg = smem + STAGES * C::STAGE_BYTES + (warp - 2) * 4096;
-        int box = 0;                                    // the staging box in turn
-        // lane's row of 32 columns into the free box (64-byte rows, 16-byte piece c at c ^ (row / 2 % 4)),
-        // once the bulk store before the last one has read it
-        auto stage = [&](const uint32_t(&pk)[16]) -> uint8_t* {
-            uint8_t* bx = stg + box * 2048;
-            box ^= 1;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                *reinterpret_cast<uint4*>(bx + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
-                    make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            return bx;
-        };
-        auto free_box = [&]() {
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-            __syncwarp();
-        };
+        // Warp: TMEM lane quarter q, 64 columns.  Its box of 32 rows x 128 bytes (128-byte swizzle) first
+        // receives the addend by TMA, then each lane turns its row into D's, then a bulk store takes it.
+        const int q = warp & 3, cb = ((warp - 2) >> 2) * 64;
+        uint8_t* box = smem + C::OFF_STG + (warp - 2) * C::BOX_BYTES;
+        uint8_t* box2 = box + 4096;
+        uint64_t* addb = &add_full[warp - 2];
+        auto at = [&](uint8_t* b, int c16) -> uint8_t* { return b + lane * 128 + ((c16 ^ (lane & 7)) << 4); };
         int lt = 0;
-        for (int t = blockIdx.x; t < ntile; t += gridDim.x, ++lt) {
+        uint32_t addph = 0;
+        bool ok = true;
+        for (int t = cid; t < p.ntile; t += ncid, ++lt) {
             const Tile ti = decode(t);
             const int buf = lt & 1;
             const int row0 = ti.m * 128 + q * 32, row = row0 + lane;
-            const int col0 = ti.n * BN + half * HC;
-            const bool row_in = row < p.rows;
-            // the addend of 32 columns, as it lies: 4 lanes a row, 8 rows an instruction; loaded a step ahead
-            uint4 ad[4];
-            auto load_add = [&](int c) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = row0 + 8 * i + (lane >> 2), cc = c + (lane & 3) * 8;
-                    ad[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < p.rows && cc < p.cols)
-                        ad[i] = __ldg(reinterpret_cast<const uint4*>(p.add + r * p.add_row + ti.g * p.add_group + cc));
-                }
+            const int col0 = ti.n * BN + cb;
+            // columns of this warp inside D (none where its rows are past the extent): uniform in the warp
+            const int ncol = row0 < p.rows ? min(64, p.cols - col0) : 0;
+            const bool add = !F32OUT && p.add && ncol > 0;
+            // the box is free once the last tile's store has read it; without an addend that is waited for
+            // as late as the first write
+            auto free_box = [&]() {
+                if (lane == 0) bulk_wait_read_all();
+                __syncwarp();
             };
-            if (!F32OUT && p.add) load_add(col0);
-            if (!wait_or_abort(&acc_full[buf], (lt >> 1) & 1, abort_flag, 0x803)) break;
+            if (add && lane == 0) {
+                bulk_wait_read_all();
+                mbar_arrive_expect_tx(addb, 4096);
+                tma_load_3d(box, &tmR, addb, col0, ti.g, row0);
+            }
+            // two columns' bias a lane (by the columns alone: warps without rows write the shared values too)
+            uint32_t bw = 0u;
+            if (!F32OUT && p.bias && col0 + 2 * lane < p.cols)
+                bw = __ldg(reinterpret_cast<const uint32_t*>(p.bias + (size_t)ti.g * p.cols + col0 + 2 * lane));
+            if (!wait_or_abort(&acc_full[buf], (lt >> 1) & 1, abort_flag, 0x803)) ok = false;
+            if (add) {                       // also on the way out: the load lands before the block ends
+                ok = wait_or_abort(addb, addph, abort_flag, 0x807) && ok;
+                if (!ok) mbar_wait(addb, addph, 0x808);
+                addph ^= 1;
+            }
+            if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            const uint32_t taddr = tmem_base + (uint32_t(q * 32) << 16) + buf * BN + half * HC;
-            // a box of 32 columns; those past the extents are not computed (uniform across the warp)
-            const int ncol = row0 < p.rows ? min(HC, p.cols - col0) : 0;
-            uint32_t ew = 0u;                           // exponents of up to four blocks of the row
-#pragma unroll 1
-            for (int c = 0; c < ncol; c += 32) {
+            // into shared memory, behind the wait: by then every warp has read the bias of the tile before
+            // last, which lay there.  The four warps of a column block write the same values.
+            float* sbias = reinterpret_cast<float*>(smem + C::OFF_BIAS) + buf * BN + cb;
+            if (!F32OUT && p.bias) *reinterpret_cast<float2*>(sbias + 2 * lane) = make_float2(bf16_lo(bw), bf16_hi(bw));
+            __syncwarp();
+            const uint32_t taddr = tmem_base + (uint32_t(q * 32) << 16) + buf * BN + cb;
+            int e2[2] = {0, 0};              // exponents of the row's two blocks
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
                 float v[32];
-                tmem_ld32(taddr + c, v);
-                const int col = col0 + c;
-                if constexpr (F32OUT) {
-                    // fp32 partial sums: 32 rows x 128 bytes, 128-byte swizzle, the warp's whole 4 KB
-                    if (lane == 0) bulk_wait_read_all();
+                if (32 * h < ncol) {
+                    tmem_ld32(taddr + 32 * h, v);
+                    if (!F32OUT && p.bias) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 w = *reinterpret_cast<const float4*>(sbias + 32 * h + 4 * i);
+                            const float2 lo = __fadd2_rn(make_float2(v[4 * i], v[4 * i + 1]), make_float2(w.x, w.y));
+                            const float2 hi = __fadd2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), make_float2(w.z, w.w));
+                            v[4 * i] = lo.x;
+                            v[4 * i + 1] = lo.y;
+                            v[4 * i + 2] = hi.x;
+                            v[4 * i + 3] = hi.y;
+                        }
+                    }
+                }
+                if (h == 1) {
+                    // the accumulator and the bias are read: the next MMAs into this buffer may start
+                    tc_fence_before();
                     __syncwarp();
+                    if (lane == 0) {
+                        if (PAIR) arrive_remote(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+                        else mbar_arrive(&acc_empty[buf]);
+                    }
+                }
+                if (32 * h >= ncol) continue;
+                if constexpr (F32OUT) {
+                    free_box();
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<float4*>(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) =
-                            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        *reinterpret_cast<float4*>(at(box, i)) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_3d(&tmO, stg, col, row0, ti.s * p.groups + ti.g);
+                        tma_store_3d(&tmO, box, col0 + 32 * h, row0, ti.s * p.groups + ti.g);
                         bulk_commit_group();
                     }
                 } else {
-                    if (p.bias) {
-                        const __nv_bfloat16* bp = p.bias + (size_t)ti.g * p.cols + col;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (col + 8 * i < p.cols) {
-                                const uint4 w = __ldg(reinterpret_cast<const uint4*>(bp + 8 * i));
-                                const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    v[8 * i + 2 * k] += bf16_lo(a[k]);
-                                    v[8 * i + 2 * k + 1] += bf16_hi(a[k]);
-                                }
-                            }
-                        }
-                    }
                     if constexpr (SAVE == LIN_KEEP_CK8) {
-                        // this lane's 32 columns are one block of its row (those past the row are zero:
-                        // their weights and bias were read as zero)
+                        // this lane's 32 columns are one block of its row (those past the row are zero: their
+                        // weights and bias were read as zero); 64 code bytes a row, 64-byte swizzle
                         uint32_t qw[8];
-                        const int e = ck8_quantize<32, 1>(v, qw);
-                        ew |= (uint32_t)(e & 0xFF) << ((c & 96) >> 2);
-                        if (row_in) {
-                            int8_t* cp = p.codes + ((size_t)row * p.groups + ti.g) * p.cols + col;
-                            if (col + 32 <= p.cols && (p.cols & 15) == 0) {
-                                *reinterpret_cast<uint4*>(cp) = make_uint4(qw[0], qw[1], qw[2], qw[3]);
-                                *reinterpret_cast<uint4*>(cp + 16) = make_uint4(qw[4], qw[5], qw[6], qw[7]);
-                            } else {
+                        e2[h] = ck8_quantize<32, 1>(v, qw);
+                        if (h == 0) free_box();
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    if (col + 8 * i < p.cols)
-                                        *reinterpret_cast<uint2*>(cp + 8 * i) = make_uint2(qw[2 * i], qw[2 * i + 1]);
-                            }
-                            // the exponents of four blocks together where they make an aligned word
-                            int8_t* ep = p.exps + ((size_t)row * p.groups + ti.g) * p.nblk + (col >> 5);
-                            if ((p.nblk & 3) == 0) {
-                                if ((c & 96) == 96 || c + 32 >= ncol) {
-                                    if ((c & 96) == 96) *reinterpret_cast<uint32_t*>(ep - 3) = ew;
-                                    else
-                                        for (int i = 0; i <= (c & 96) >> 5; ++i)
-                                            ep[i - ((c & 96) >> 5)] = (int8_t)(ew >> (8 * i));
-                                    ew = 0u;
-                                }
-                            } else {
-                                *ep = (int8_t)e;
-                            }
-                        }
+                        for (int i = 0; i < 2; ++i)
+                            *reinterpret_cast<uint4*>(box2 + lane * 64 + (((2 * h + i) ^ ((lane >> 1) & 3)) << 4)) =
+                                make_uint4(qw[4 * i], qw[4 * i + 1], qw[4 * i + 2], qw[4 * i + 3]);
                     }
-                    uint32_t pk[16];
                     if constexpr (SAVE == LIN_KEEP_FULL) {
+                        if (h == 0) free_box();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-                        free_box();
-                        const uint8_t* bx = stage(pk);
-                        if (lane == 0) {
-                            tma_store_3d(&tmZ, bx, col, ti.g, row0);
-                            bulk_commit_group();
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<uint4*>(at(box2, 4 * h + i)) =
+                                make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                                           pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
                     }
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -389,50 +445,78 @@ __global__ void __launch_bounds__(LinCfg<BN, SAVE>::NTHREADS, 1)
                         v[2 * i] = o.x;
                         v[2 * i + 1] = o.y;
                     }
-                    free_box();
-                    if (p.add) {
-                        // through the free box to the lane that owns the row
-                        uint8_t* bx = stg + box * 2048;
+                    if (SAVE == LIN_KEEP_NOTHING && !add && h == 0) free_box();
+                    if (add) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int r = 8 * i + (lane >> 2), cc = lane & 3;
-                            *reinterpret_cast<uint4*>(bx + r * 64 + ((cc ^ ((r >> 1) & 3)) << 4)) = ad[i];
-                        }
-                        __syncwarp();
-                        if (c + 32 < ncol) load_add(col + 32);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint4 w = *reinterpret_cast<const uint4*>(bx + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
+                            const uint4 w = *reinterpret_cast<const uint4*>(at(box, 4 * h + i));
                             const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                v[8 * i + 2 * k] += bf16_lo(a[k]);
-                                v[8 * i + 2 * k + 1] += bf16_hi(a[k]);
+                                const float2 r = __fadd2_rn(make_float2(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]),
+                                                            make_float2(bf16_lo(a[k]), bf16_hi(a[k])));
+                                v[8 * i + 2 * k] = r.x;
+                                v[8 * i + 2 * k + 1] = r.y;
                             }
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-                    const uint8_t* bx = stage(pk);
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4*>(at(box, 4 * h + i)) =
+                            make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                                       pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+                }
+            }
+            if constexpr (!F32OUT) {
+                if (ncol > 0) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
                     if (lane == 0) {
-                        if constexpr (A_MN) tma_store_3d(&tmO, bx, col, row0, ti.g);   // dW: [bank][rows][columns]
-                        else tma_store_3d(&tmO, bx, col, ti.g, row0);                   // [rows][bank][columns]
+                        if constexpr (OUT_MAT) tma_store_3d(&tmO, box, col0, row0, ti.g);
+                        else tma_store_3d(&tmO, box, col0, ti.g, row0);
+                        if constexpr (SAVE == LIN_KEEP_FULL) tma_store_3d(&tmZ, box2, col0, ti.g, row0);
+                        if constexpr (SAVE == LIN_KEEP_CK8)
+                            if ((p.cols & 15) == 0) tma_store_3d(&tmZ, box2, col0, ti.g, row0);
                         bulk_commit_group();
+                    }
+                    if constexpr (SAVE == LIN_KEEP_CK8) {
+                        if (p.cols & 15) {   // rows that are no multiple of 16 bytes have no tensor map: 8 at a time
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int r = 8 * i + (lane >> 2), c16 = lane & 3;
+                                const uint4 w = *reinterpret_cast<const uint4*>(box2 + r * 64 + ((c16 ^ ((r >> 1) & 3)) << 4));
+                                int8_t* cp = p.codes + ((size_t)(row0 + r) * p.groups + ti.g) * p.cols + col0 + 16 * c16;
+                                if (row0 + r < p.rows) {
+                                    if (16 * c16 < ncol) *reinterpret_cast<uint2*>(cp) = make_uint2(w.x, w.y);
+                                    if (16 * c16 + 8 < ncol) *reinterpret_cast<uint2*>(cp + 8) = make_uint2(w.z, w.w);
+                                }
+                            }
+                        }
+                        if (row < p.rows) {
+                            int8_t* ep = p.exps + ((size_t)row * p.groups + ti.g) * p.nblk + (col0 >> 5);
+                            if ((p.nblk & 1) == 0) {
+                                *reinterpret_cast<uint16_t*>(ep) = (uint16_t)((e2[0] & 0xFF) | (e2[1] & 0xFF) << 8);
+                            } else {
+                                ep[0] = (int8_t)e2[0];
+                                if (ncol > 32) ep[1] = (int8_t)e2[1];
+                            }
+                        }
                     }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[buf]);
         }
         if (lane == 0) bulk_wait_all();
         __syncwarp();
     }
     tc_fence_before();
-    __syncthreads();
+    // pair mode: neither CTA releases its tensor memory or exits while the other may still arrive on its
+    // barriers or be the target of the pair's MMAs
+    if (PAIR) cluster_sync_all();
+    else __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, C::TMEM_COLS);
+        if (PAIR) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+        else tmem_dealloc(tmem_base, C::TMEM_COLS);
     }
 }
 

@@ -66,46 +66,17 @@ struct NormBlock {
     static constexpr int ROWS = THREADS / G;
 };
 
-// Element offset of the vector at column c of row (b, bank) in x's tensor.
-__device__ __forceinline__ size_t norm_off(const RowMap& m, int b, int bank, int c) { return row_elem(m, b, bank, c); }
-
-// Forward: one row per G threads, NV vectors of V values a thread.
+// A row's statistics, checkpoint and output from its z in registers (the forward after its loads).
 template <typename T, int V, int NV, int G>
-__global__ void __launch_bounds__(NormBlock<G>::THREADS) ln_fwd_kernel(const NormParams p) {
-    __shared__ float red[2 * (G > 32 ? G / 32 : 1)];
-    int turn = 0;
+__device__ __forceinline__ void ln_fwd_row(const NormParams& p, const float (&z)[NV][V], bool live, long long row,
+                                           int gl, float* red, int& turn) {
     const int W = p.map.W;
-    const int gl = threadIdx.x % G;
-    const long long nrows = (long long)p.B * p.map.banks;
-    const long long row = (long long)blockIdx.x * NormBlock<G>::ROWS + threadIdx.x / G;
-    const bool live = row < nrows;          // lanes past the last row take part in the shuffles
-    const int b = live ? (int)(row / p.map.banks) : 0;
-    const int bank = live ? (int)(row - (long long)b * p.map.banks) : 0;
-    const size_t ro = (size_t)(live ? row : 0) * W;
-    Pack<T, V> xw[NV], rw[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (gl + G * i) * V;
-        xw[i].zero();
-        rw[i].zero();
-        if (live && c < W) {
-            xw[i].load((const T*)p.x + norm_off(p.map, b, bank, c));
-            if (p.res) rw[i].load((const T*)p.res + ro + c);
-        }
-    }
-    float z[NV][V];
+    const size_t ro = (size_t)row * W;
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        float r[V];
-        xw[i].get(z[i]);
-        rw[i].get(r);
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            z[i][k] += r[k];
-            sum += z[i][k];
-        }
-    }
+        for (int k = 0; k < V; ++k) sum += z[i][k];
     const float mu = row_sum<G>(sum, red, turn) / (float)W;
     float sq = 0.f;
 #pragma unroll
@@ -160,6 +131,42 @@ __global__ void __launch_bounds__(NormBlock<G>::THREADS) ln_fwd_kernel(const Nor
     }
 }
 
+// Forward: one row per G threads, NV vectors of V values a thread.
+template <typename T, int V, int NV, int G>
+__global__ void __launch_bounds__(NormBlock<G>::THREADS) ln_fwd_kernel(const NormParams p) {
+    __shared__ float red[2 * (G > 32 ? G / 32 : 1)];
+    int turn = 0;
+    const int W = p.map.W;
+    const int gl = threadIdx.x % G;
+    const long long nrows = (long long)p.B * p.map.banks;
+    const long long row = (long long)blockIdx.x * NormBlock<G>::ROWS + threadIdx.x / G;
+    const bool live = row < nrows;          // lanes past the last row take part in the shuffles
+    const int b = live ? (int)(row / p.map.banks) : 0;
+    const int bank = live ? (int)(row - (long long)b * p.map.banks) : 0;
+    const size_t ro = (size_t)(live ? row : 0) * W;
+    Pack<T, V> xw[NV], rw[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (gl + G * i) * V;
+        xw[i].zero();
+        rw[i].zero();
+        if (live && c < W) {
+            xw[i].load((const T*)p.x + row_elem(p.map, b, bank, c));
+            if (p.res) rw[i].load((const T*)p.res + ro + c);
+        }
+    }
+    float z[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float r[V];
+        xw[i].get(z[i]);
+        rw[i].get(r);
+#pragma unroll
+        for (int k = 0; k < V; ++k) z[i][k] += r[k];
+    }
+    ln_fwd_row<T, V, NV, G>(p, z, live, live ? row : 0, gl, red, turn);
+}
+
 // What the backward pass reads of one row: dy, and x (+ residual) or the checkpoint of their sum.
 template <typename T, int V, int NV, bool CK>
 struct NormRow {
@@ -191,7 +198,7 @@ struct NormRow {
                     ck8_load<V>(p.codes + ro + c, q[i]);
                     e[i] = __ldg(p.exps + row * nblk + c / kCk8Block);
                 } else {
-                    xw[i].load((const T*)p.x + norm_off(p.map, b, bank, c));
+                    xw[i].load((const T*)p.x + row_elem(p.map, b, bank, c));
                     if (p.res) rw[i].load((const T*)p.res + ro + c);
                 }
             }
@@ -312,18 +319,39 @@ __global__ void __launch_bounds__(NormBlock<G>::THREADS) ln_bwd_kernel(const Nor
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int k = 0; k < V; ++k) dg[i][k] = db[i][k] = 0.f;
-    for (long long base = (long long)blockIdx.x * ROWS; base < nrows; base += (long long)gridDim.x * ROWS) {
-        const long long row = base + threadIdx.x / G;
-        const bool live = row < nrows;      // a group without a row works on zeros, which add nothing
-        const int b = live ? (int)(row / p.map.banks) : 0;
-        const int bank = live ? (int)(row - (long long)b * p.map.banks) : 0;
-        NormRow<T, V, NV, CK> r;
-        const float mu = live ? __ldg(p.mean + row) : 0.f, rs = live ? __ldg(p.rstd + row) : 0.f;
-        r.template load<G>(p, live, row, b, bank, gl);
-        ln_bwd_row<T, V, NV, G, CK>(p, r, mu, rs, gl, red, turn, dg, db, [&](int c, const float(&d)[V]) {
-            if (!live) return;
-            Pack<T, V>::store((T*)p.dx + norm_off(p.map, b, bank, c), d);
-            if (mixed && p.dres) Pack<T, V>::store((T*)p.dres + (size_t)row * W + c, d);
+    // the next row's loads are in flight while this one is worked on
+    struct At {
+        long long row;
+        bool live;
+        int b, bank;
+        float mu, rs;
+    };
+    auto at = [&](long long base) -> At {
+        At a;
+        a.row = base + threadIdx.x / G;
+        a.live = a.row < nrows;             // a group without a row works on zeros, which add nothing
+        a.b = a.live ? (int)(a.row / p.map.banks) : 0;
+        a.bank = a.live ? (int)(a.row - (long long)a.b * p.map.banks) : 0;
+        a.mu = a.live ? __ldg(p.mean + a.row) : 0.f;
+        a.rs = a.live ? __ldg(p.rstd + a.row) : 0.f;
+        return a;
+    };
+    const long long step = (long long)gridDim.x * ROWS;
+    long long base = (long long)blockIdx.x * ROWS;
+    NormRow<T, V, NV, CK> rn;
+    At an = at(base);
+    rn.template load<G>(p, an.live, an.row, an.b, an.bank, gl);
+    for (; base < nrows; base += step) {
+        const NormRow<T, V, NV, CK> r = rn;
+        const At a = an;
+        if (base + step < nrows) {
+            an = at(base + step);
+            rn.template load<G>(p, an.live, an.row, an.b, an.bank, gl);
+        }
+        ln_bwd_row<T, V, NV, G, CK>(p, r, a.mu, a.rs, gl, red, turn, dg, db, [&](int c, const float(&d)[V]) {
+            if (!a.live) return;
+            Pack<T, V>::store((T*)p.dx + row_elem(p.map, a.b, a.bank, c), d);
+            if (mixed && p.dres) Pack<T, V>::store((T*)p.dres + (size_t)a.row * W + c, d);
         });
     }
     if (p.part) ln_store_partials<V, NV, G>(p, sm, gl, dg, db);
@@ -401,6 +429,301 @@ __global__ void __launch_bounds__(THREADS) ln_bwd_self_kernel(const NormParams p
     }
 }
 
+// ------------------------------------------------------------------ whole samples: LN(Mix(X) + X)
+// With T = H and X as the residual too, everything a sample's rows read is the sample itself, one
+// contiguous piece of memory.  Blocks bring samples into shared memory by bulk copies, a ring of NB
+// slots ahead of the arithmetic, so that the scattered reads of the Mix view (pieces of dh columns, one
+// per token) cost shared-memory cycles instead of L1 lookups, and loads stay in flight while rows are
+// worked on.  A token row of a slot is `ld` bytes, padded so that ld = dh * esz modulo 128: the pieces
+// of 8 lanes then fall into different banks.
+struct SampleRing {
+    uint8_t* base;             // slots, then one barrier each
+    uint64_t* full;
+    uint32_t slot_bytes;
+    int nb;
+};
+
+// Token rows of one sample (rows x bytes each, contiguous in memory) into a slot.  One thread.
+__device__ __forceinline__ void sample_load(const SampleRing& r, int slot, const void* src, int rows, uint32_t bytes,
+                                            uint32_t ld) {
+    uint64_t* bar = r.full + slot;
+    mbar_arrive_expect_tx(bar, rows * bytes);
+    uint8_t* dst = r.base + slot * r.slot_bytes;
+    for (int t = 0; t < rows; ++t) bulk_load(dst + t * ld, (const uint8_t*)src + (size_t)t * bytes, bytes, bar);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void smem_vec(const uint8_t* p, float (&v)[V]) {
+    Pack<T, V> w;
+    w.w = *reinterpret_cast<const decltype(w.w)*>(p);
+    w.get(v);
+}
+
+template <typename T, int V, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS) ln_sample_fwd_kernel(const NormParams p, uint32_t ld, int nb) {
+    extern __shared__ __align__(128) uint8_t sms[];
+    __shared__ uint64_t bars[8];
+    const int W = p.map.W, H = p.map.banks, dh = p.map.dh;
+    const uint32_t bytes = W * sizeof(T);
+    const SampleRing ring{sms, bars, H * ld, nb};
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int turn = 0;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < nb; ++i) mbar_init(&bars[i], 1);
+        fence_barrier_init();
+    }
+    __syncthreads();
+    const T* x = (const T*)p.x;
+    const size_t per = (size_t)H * W;
+    // load i of this block is sample blockIdx.x + i * gridDim.x, in slot i % nb
+    const int mine = blockIdx.x < p.B ? (p.B - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+    if (threadIdx.x == 0)
+        for (int i = 0; i < nb && i < mine; ++i)
+            sample_load(ring, i, x + (blockIdx.x + (size_t)i * gridDim.x) * per, H, bytes, ld);
+    // byte offsets of this lane's vectors in a token row, and of the Mix view's pieces
+    int moff[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (lane + 32 * i) * V, t = c / dh;
+        moff[i] = t * (int)ld + (c - t * dh) * (int)sizeof(T);
+    }
+    int slot = 0;
+    uint32_t ph = 0;
+    int done = 0;
+    for (; done < mine; ++done) {
+        const bool ok = mbar_wait(&bars[slot], ph, 0x810);
+        if (!__syncthreads_and(ok)) break;
+        const uint8_t* sx = sms + slot * ring.slot_bytes;
+        const long long b = blockIdx.x + (long long)done * gridDim.x;
+        for (int h = warp; h < H; h += THREADS / 32) {
+            float z[NV][V];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (lane + 32 * i) * V;
+#pragma unroll
+                for (int k = 0; k < V; ++k) z[i][k] = 0.f;
+                if (c < W) {
+                    float r[V];
+                    smem_vec<T, V>(sx + moff[i] + h * dh * (int)sizeof(T), z[i]);
+                    smem_vec<T, V>(sx + h * ld + c * (int)sizeof(T), r);
+#pragma unroll
+                    for (int k = 0; k < V; ++k) z[i][k] += r[k];
+                }
+            }
+            ln_fwd_row<T, V, NV, 32>(p, z, true, b * H + h, lane, nullptr, turn);
+        }
+        __syncthreads();
+        if (threadIdx.x == 0 && done + nb < mine)
+            sample_load(ring, slot, x + (b + (size_t)nb * gridDim.x) * per, H, bytes, ld);
+        if (++slot == nb) { slot = 0; ph ^= 1; }
+    }
+    if (done < mine && threadIdx.x == 0)    // given up: the loads in flight land before the block ends
+        for (int i = 0; i < nb && done + i < mine; ++i) {
+            mbar_wait(&bars[slot], ph, 0x811);
+            if (++slot == nb) { slot = 0; ph ^= 1; }
+        }
+}
+
+// Backward of the same, dX = dz + Revert(dz).  Mix(X) + X is symmetric under exchange of a token and a
+// head (its element (row h, column t * dh + j) is X[t][h * dh + j] + X[h][t * dh + j]), and so is dX:
+// dX[t][h * dh + j] = dz[t][h * dh + j] + dz[h][t * dh + j] = dX[h][t * dh + j].  A sample takes two
+// slots (X or the checkpoint's codes, and dy).  First its rows' two means, with dgain and dbias on the
+// way, a warp a row; then every pair of elements once, from the same shared memory: dz is never stored.
+template <typename T, int V, int NV, bool CK, int THREADS>
+__global__ void __launch_bounds__(THREADS) ln_sample_bwd_kernel(const NormParams p, uint32_t ld, uint32_t ldc, int nb) {
+    extern __shared__ __align__(128) uint8_t sms[];
+    __shared__ uint64_t bars[8];
+    constexpr int NW = THREADS / 32;
+    const int W = p.map.W, H = p.map.banks, dh = p.map.dh;
+    const int nblk = (W + kCk8Block - 1) / kCk8Block;
+    constexpr int ES = sizeof(T);
+    const uint32_t bytes = W * ES;
+    const SampleRing ring{sms, bars, H * ld, nb};
+    float4* rowc = reinterpret_cast<float4*>(sms + (size_t)nb * ring.slot_bytes);   // [H] {rs, mu, -rs m1, -rs^2 m2}
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int turn = 0;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < nb; ++i) mbar_init(&bars[i], 1);
+        fence_barrier_init();
+    }
+    __syncthreads();
+    const size_t per = (size_t)H * W;
+    const int mine = blockIdx.x < p.B ? (p.B - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+    // load 2 i is sample i's X (or codes), load 2 i + 1 its dy; load l goes to slot l % nb
+    auto load = [&](int l, int slot) {
+        const size_t b = blockIdx.x + (size_t)(l >> 1) * gridDim.x;
+        if (l & 1) sample_load(ring, slot, (const T*)p.dy + b * per, H, bytes, ld);
+        else if (CK) sample_load(ring, slot, p.codes + b * per, H, W, ldc);
+        else sample_load(ring, slot, (const T*)p.x + b * per, H, bytes, ld);
+    };
+    if (threadIdx.x == 0)
+        for (int l = 0; l < nb && l < 2 * mine; ++l) load(l, l);
+    float dg[NV][V], db[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) dg[i][k] = db[i][k] = 0.f;
+    int moff[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (lane + 32 * i) * V, t = c / dh;
+        moff[i] = t * (int)ld + (c - t * dh) * ES;
+    }
+    const int vpd = dh / V;                                // vectors of a piece
+    const int npair = (H + 1) / 2 * (H + 1) * vpd;
+    int slot = 0;
+    uint32_t ph = 0;
+    int done = 0;
+    for (; done < mine; ++done) {
+        const int slot2 = slot + 1 == nb ? 0 : slot + 1;
+        const bool ok = mbar_wait(&bars[slot], ph, 0x812) && mbar_wait(&bars[slot2], slot2 ? ph : ph ^ 1, 0x813);
+        if (!__syncthreads_and(ok)) break;
+        const uint8_t* sx = sms + slot * ring.slot_bytes;
+        const uint8_t* sd = sms + slot2 * ring.slot_bytes;
+        const long long b = blockIdx.x + (long long)done * gridDim.x;
+        const int8_t* ex = CK ? p.exps + b * H * nblk : nullptr;
+        for (int h = warp; h < H; h += NW) {
+            const float mu = __ldg(p.mean + b * H + h), rs = __ldg(p.rstd + b * H + h);
+            float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (lane + 32 * i) * V;
+                if (c < W) {
+                    float n[V], d[V], g[V];
+                    if constexpr (CK) {
+                        uint32_t q[(V + 3) / 4];
+                        if constexpr (V == 8) {
+                            const uint2 w = *reinterpret_cast<const uint2*>(sx + h * ldc + c);
+                            q[0] = w.x;
+                            q[1] = w.y;
+                        } else {
+                            q[0] = *reinterpret_cast<const uint32_t*>(sx + h * ldc + c);
+                        }
+                        ck8_values<V>(q, ck8_scale(__ldg(ex + h * nblk + c / kCk8Block)), n);
+                    } else {
+                        float r[V];
+                        smem_vec<T, V>(sx + moff[i] + h * dh * ES, n);
+                        smem_vec<T, V>(sx + h * ld + c * ES, r);
+#pragma unroll
+                        for (int k = 0; k < V; ++k) n[k] += r[k];
+                    }
+                    smem_vec<T, V>(sd + h * ld + c * ES, d);
+                    norm_gain<T, V>(p, c, g);
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        n[k] = (n[k] - mu) * rs;
+                        dg[i][k] = fmaf(d[k], n[k], dg[i][k]);
+                        db[i][k] += d[k];
+                        const float dn = d[k] * g[k];
+                        s1 += dn;
+                        s2 = fmaf(dn, n[k], s2);
+                    }
+                }
+            }
+            const float m1 = row_sum<32>(s1, nullptr, turn) / (float)W;
+            const float m2 = row_sum<32>(s2, nullptr, turn) / (float)W;
+            if (lane == 0) rowc[h] = make_float4(rs, mu, -rs * m1, -rs * rs * m2);
+        }
+        __syncthreads();
+        // pairs (t <= h): rows i and H-1-i of the triangle together are H + 1 pieces
+        T* out = (T*)p.dx + b * per;
+        for (int u = threadIdx.x; u < npair; u += THREADS) {
+            const int j = u % vpd * V;
+            const int k2 = u / vpd;
+            const int i = k2 / (H + 1), k = k2 - i * (H + 1);
+            int t, h;
+            if (k < H - i) {
+                t = i;
+                h = i + k;
+            } else {
+                t = H - 1 - i;
+                h = t + k - (H - i);
+                if (t == i) continue;                      // odd H: the middle row is its own partner
+            }
+            const int ca = h * dh + j, cb = t * dh + j;
+            float za[V], zb[V], da[V], dd[V], ga[V], gb[V];
+            if constexpr (CK) {
+                uint32_t q[(V + 3) / 4];
+                auto codes = [&](int r, int c, float(&v)[V]) {
+                    if constexpr (V == 8) {
+                        const uint2 w = *reinterpret_cast<const uint2*>(sx + r * ldc + c);
+                        q[0] = w.x;
+                        q[1] = w.y;
+                    } else {
+                        q[0] = *reinterpret_cast<const uint32_t*>(sx + r * ldc + c);
+                    }
+                    ck8_values<V>(q, ck8_scale(__ldg(ex + r * nblk + c / kCk8Block)), v);
+                };
+                codes(t, ca, za);
+                codes(h, cb, zb);
+            } else {
+                smem_vec<T, V>(sx + t * ld + ca * ES, za);
+                smem_vec<T, V>(sx + h * ld + cb * ES, zb);
+#pragma unroll
+                for (int e = 0; e < V; ++e) za[e] = zb[e] = za[e] + zb[e];
+            }
+            smem_vec<T, V>(sd + t * ld + ca * ES, da);
+            smem_vec<T, V>(sd + h * ld + cb * ES, dd);
+            norm_gain<T, V>(p, ca, ga);
+            norm_gain<T, V>(p, cb, gb);
+            const float4 ra = rowc[t], rb = rowc[h];
+            float o[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float a = fmaf(za[e] - ra.y, ra.w, fmaf(da[e] * ga[e], ra.x, ra.z));
+                const float c = fmaf(zb[e] - rb.y, rb.w, fmaf(dd[e] * gb[e], rb.x, rb.z));
+                o[e] = a + c;
+            }
+            Pack<T, V>::store(out + (size_t)t * W + ca, o);
+            if (t != h) Pack<T, V>::store(out + (size_t)h * W + cb, o);
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            if (2 * done + nb < 2 * mine) load(2 * done + nb, slot);
+            if (2 * done + 1 + nb < 2 * mine) load(2 * done + 1 + nb, slot2);
+        }
+        slot += 2;
+        if (slot >= nb) { slot -= nb; ph ^= 1; }
+    }
+    if (done < mine) {                       // given up: the loads in flight land before the block ends
+        if (threadIdx.x == 0)
+            for (int l = 2 * done; l < 2 * mine && l < 2 * done + nb; ++l) {
+                mbar_wait(&bars[slot], ph, 0x814);
+                if (++slot == nb) { slot = 0; ph ^= 1; }
+            }
+        return;
+    }
+    if (!p.part) return;
+    // the warps' sums of dgain and dbias in a fixed order, through the slots (every read is behind the
+    // last barrier): `room` warps' rows at a time
+    float* sm = reinterpret_cast<float*>(sms);
+    float* out = p.part + (size_t)blockIdx.x * 2 * W;
+    const int fit = (int)((size_t)nb * ring.slot_bytes / (W * sizeof(float)));
+    const int room = fit < NW ? fit : NW;
+    for (int which = 0; which < 2; ++which) {
+        for (int w0 = 0; w0 < NW; w0 += room) {
+            __syncthreads();
+            if (warp >= w0 && warp < w0 + room) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int c = (lane + 32 * i) * V;
+                    if (c < W) {
+#pragma unroll
+                        for (int k = 0; k < V; ++k) sm[(warp - w0) * W + c + k] = which == 0 ? dg[i][k] : db[i][k];
+                    }
+                }
+            }
+            __syncthreads();
+            const int n = min(room, NW - w0);
+            for (int c = threadIdx.x; c < W; c += THREADS) {
+                float s = w0 == 0 ? 0.f : out[which * W + c];
+                for (int r = 0; r < n; ++r) s += sm[r * W + c];
+                out[which * W + c] = s;
+            }
+        }
+    }
+}
+
 // out0[c] = sum over n of part[n][0][c], out1[c] of part[n][1][c] (either may be NULL), fixed order: 8
 // slices of the n partials per column, then the slices.  Grid: ceil(2 W / 32) blocks of 32 x 8 threads.
 template <typename T>
@@ -425,8 +748,8 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const float* __restric
 
 // ------------------------------------------------------------------ launchers
 // Rows of W columns in vectors of V: the threads per row G and vectors per thread NV.
-#define TM_NORM_SIZES_8(X) X(8, 1, 8) X(8, 1, 16) X(8, 1, 32) X(8, 2, 32) X(8, 3, 32) X(8, 4, 32) X(8, 4, 128) X(8, 4, 512)
-#define TM_NORM_SIZES_4(X) X(4, 1, 8) X(4, 1, 16) X(4, 1, 32) X(4, 2, 32) X(4, 4, 32) X(4, 8, 32) X(4, 8, 128) X(4, 8, 512)
+#define TM_NORM_SIZES_8(X) X(8, 1, 8) X(8, 1, 16) X(8, 3, 8) X(8, 1, 32) X(8, 3, 16) X(8, 2, 32) X(8, 3, 32) X(8, 4, 32) X(8, 4, 128) X(8, 4, 512)
+#define TM_NORM_SIZES_4(X) X(4, 1, 8) X(4, 1, 16) X(4, 1, 32) X(4, 3, 16) X(4, 2, 32) X(4, 3, 32) X(4, 4, 32) X(4, 8, 32) X(4, 8, 128) X(4, 8, 512)
 #define TM_NORM_SIZES_1(X) X(1, 4, 32) X(1, 16, 32) X(1, 16, 128) X(1, 32, 512)
 
 int norm_max_width() { return 16384; }
@@ -449,8 +772,89 @@ static cudaError_t launch_ln_fwd_t(const NormParams& p, int vec, cudaStream_t st
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_ln_fwd(int dtype, const NormParams& p, cudaStream_t st) {
+// ---- sample kernels (X the residual too): the ring's slots and block size
+constexpr size_t kSampleSmem = 225 * 1024;
+// bytes of a padded token row (piece: bytes of dh columns; a multiple of 16)
+static uint32_t sample_ld(uint32_t bytes, uint32_t piece) {
+    if (piece < 16) piece = 16;
+    return bytes + (piece + 128 - bytes % 128) % 128;
+}
+// Slots for `need` at least and 4 at most: two blocks an SM where that leaves each the slots it wants.
+static int sample_slots(size_t slot, size_t extra, int need) {
+    const size_t half = kSampleSmem / 2 - extra, whole = kSampleSmem - extra;
+    int nb = (int)(half / slot);
+    if (nb < need + 1) nb = (int)(whole / slot);
+    return nb < need ? 0 : (nb > 4 ? 4 : nb);
+}
+// Samples of at least 8 KB; smaller ones leave a block's threads idle, and the row kernels take them.
+constexpr size_t kSampleLeast = 8 * 1024;
+
+template <class K>
+static cudaError_t norm_resident(K kern, int threads, size_t smem_most, std::atomic<int>* cache, int* per_sm);
+static long long norm_bwd_blocks(long long nrows, int rows_per_block, int per_sm, size_t smem, int sms);
+
+template <typename T, int V, int NV>
+static cudaError_t launch_sample_fwd(const NormParams& p, uint32_t ld, int nb, int sms, cudaStream_t st) {
+    constexpr int THREADS = 512;
+    auto kern = ln_sample_fwd_kernel<T, V, NV, THREADS>;
+    static std::atomic<int> cache[64];
+    int per_sm = 0;
+    cudaError_t e = norm_resident(kern, THREADS, kSampleSmem, cache, &per_sm);
+    if (e != cudaSuccess) return e;
+    const size_t smem = (size_t)nb * p.map.banks * ld;
+    kern<<<(unsigned)norm_bwd_blocks(p.B, 1, per_sm, smem, sms), THREADS, smem, st>>>(p, ld, nb);
+    return cudaGetLastError();
+}
+template <typename T>
+static cudaError_t launch_sample_fwd_t(const NormParams& p, uint32_t ld, int nb, int sms, cudaStream_t st) {
+    constexpr int V = sizeof(T) == 2 ? 8 : 4;
+    const int nv = (p.map.W + 32 * V - 1) / (32 * V);
+    if (nv == 1) return launch_sample_fwd<T, V, 1>(p, ld, nb, sms, st);
+    if (nv == 2) return launch_sample_fwd<T, V, 2>(p, ld, nb, sms, st);
+    if (nv == 3) return launch_sample_fwd<T, V, 3>(p, ld, nb, sms, st);
+    if (nv == 4) return launch_sample_fwd<T, V, 4>(p, ld, nb, sms, st);
+    if constexpr (V == 4) return launch_sample_fwd<T, V, 8>(p, ld, nb, sms, st);
+    return cudaErrorInvalidValue;
+}
+
+template <typename T, int V, int NV, bool CK>
+static cudaError_t launch_sample_bwd(const NormParams& p, uint32_t ld, uint32_t ldc, int nb, int sms, int* nblk,
+                                     cudaStream_t st) {
+    constexpr int THREADS = 512;
+    auto kern = ln_sample_bwd_kernel<T, V, NV, CK, THREADS>;
+    static std::atomic<int> cache[64];
+    int per_sm = 0;
+    cudaError_t e = norm_resident(kern, THREADS, kSampleSmem, cache, &per_sm);
+    if (e != cudaSuccess) return e;
+    const size_t smem = (size_t)nb * p.map.banks * ld + p.map.banks * sizeof(float4);
+    const long long grid = norm_bwd_blocks(p.B, 1, per_sm, smem, sms);
+    *nblk = (int)grid;
+    kern<<<(unsigned)grid, THREADS, smem, st>>>(p, ld, ldc, nb);
+    return cudaGetLastError();
+}
+template <typename T, bool CK>
+static cudaError_t launch_sample_bwd_t(const NormParams& p, uint32_t ld, uint32_t ldc, int nb, int sms, int* nblk,
+                                       cudaStream_t st) {
+    constexpr int V = sizeof(T) == 2 ? 8 : 4;
+    const int nv = (p.map.W + 32 * V - 1) / (32 * V);
+    if (nv == 1) return launch_sample_bwd<T, V, 1, CK>(p, ld, ldc, nb, sms, nblk, st);
+    if (nv == 2) return launch_sample_bwd<T, V, 2, CK>(p, ld, ldc, nb, sms, nblk, st);
+    if (nv == 3) return launch_sample_bwd<T, V, 3, CK>(p, ld, ldc, nb, sms, nblk, st);
+    if (nv == 4) return launch_sample_bwd<T, V, 4, CK>(p, ld, ldc, nb, sms, nblk, st);
+    if constexpr (V == 4) return launch_sample_bwd<T, V, 8, CK>(p, ld, ldc, nb, sms, nblk, st);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_ln_fwd(int dtype, const NormParams& p, int sms, cudaStream_t st) {
     ProfileScope ps_("layer_norm", st);
+    const int esz = dtype == 1 ? 2 : 4;
+    if (p.map.layout == 1 && p.res == p.x && p.map.T == p.map.banks && p.map.W <= 1024 &&
+        (size_t)p.map.banks * p.map.W * esz >= kSampleLeast) {
+        const uint32_t ld = sample_ld(p.map.W * esz, p.map.dh * esz);
+        const int nb = sample_slots((size_t)p.map.banks * ld, 0, 1);
+        if (nb) return dtype == 1 ? launch_sample_fwd_t<__nv_bfloat16>(p, ld, nb, sms, st)
+                                  : launch_sample_fwd_t<float>(p, ld, nb, sms, st);
+    }
     const int vec = norm_vec(dtype, p.map.W);
     return dtype == 1 ? launch_ln_fwd_t<__nv_bfloat16>(p, vec, st) : launch_ln_fwd_t<float>(p, vec, st);
 }
@@ -564,8 +968,17 @@ cudaError_t launch_ln_bwd(int dtype, const NormParams& p, bool self, void* dgain
     cudaError_t e;
     {
         ProfileScope ps_("layer_norm_bwd", st);
-        const int vec = norm_vec(dtype, p.map.W);
-        if (self)
+        const int vec = norm_vec(dtype, p.map.W), esz = dtype == 1 ? 2 : 4;
+        const uint32_t ld = sample_ld(p.map.W * esz, p.map.dh * esz), ldc = sample_ld(p.map.W, p.map.dh);
+        int nb = 0;
+        if (self && (size_t)p.map.banks * p.map.W * esz >= kSampleLeast && (!ck || p.map.W % 16 == 0))
+            nb = sample_slots((size_t)p.map.banks * ld, p.map.banks * sizeof(float4), 2);
+        if (nb)
+            e = dtype == 1 ? (ck ? launch_sample_bwd_t<__nv_bfloat16, true>(p, ld, ldc, nb, sms, &nblk, st)
+                                 : launch_sample_bwd_t<__nv_bfloat16, false>(p, ld, ldc, nb, sms, &nblk, st))
+                           : (ck ? launch_sample_bwd_t<float, true>(p, ld, ldc, nb, sms, &nblk, st)
+                                 : launch_sample_bwd_t<float, false>(p, ld, ldc, nb, sms, &nblk, st));
+        else if (self)
             e = dtype == 1 ? (ck ? launch_ln_self_t<__nv_bfloat16, true>(p, sms, &nblk, st)
                                  : launch_ln_self_t<__nv_bfloat16, false>(p, sms, &nblk, st))
                            : (ck ? launch_ln_self_t<float, true>(p, sms, &nblk, st)

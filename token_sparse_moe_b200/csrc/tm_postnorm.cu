@@ -10,13 +10,14 @@ struct Span {
     const void* p;
     size_t bytes;
     bool out;
+    unsigned align = 16;
 };
-// Every span present is 16-byte aligned, and no output overlaps another span.
+// Every span present is aligned, and no output overlaps another span.
 template <int N>
 bool spans_ok(const Span (&s)[N]) {
     for (int i = 0; i < N; ++i) {
         if (!s[i].p) continue;
-        if (!al16(s[i].p)) return false;
+        if ((reinterpret_cast<uintptr_t>(s[i].p) & (s[i].align - 1)) != 0) return false;
         for (int j = 0; j < N; ++j) {
             if (i == j || !s[j].p || !s[i].out) continue;
             const uintptr_t a = (uintptr_t)s[i].p, b = (uintptr_t)s[j].p;
@@ -117,6 +118,16 @@ bool map_mats(CUtensorMap* m, const void* base, int banks, int R, int W, uint32_
               CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
     return map_3d(m, base, W, R, W, banks, (uint64_t)R * W, b0, b1, 1, swz);
 }
+bool map_codes(CUtensorMap* m, const void* base, int B, int banks, int W) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)W, (cuuint64_t)banks, (cuuint64_t)B};
+    cuuint64_t strides[2] = {(cuuint64_t)W, (cuuint64_t)banks * W};
+    cuuint32_t box[3] = {64, 1, 32}, es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 bool map_mats_f32(CUtensorMap* m, const void* base, uint64_t mats, int R, int W) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
@@ -128,30 +139,34 @@ bool map_mats_f32(CUtensorMap* m, const void* base, uint64_t mats, int R, int W)
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tile width and contraction splits of one contraction.  Estimated time in units of one 64-deep slab of
-// a 256-wide tile (about 256 tensor-core cycles): full waves of tiles times slabs, plus a tile's fill
-// and epilogue; a 128-wide tile takes somewhat more than half (its A traffic is not halved); a split
-// adds the partial sums' way out and back through memory and one more launch.
+// Tile shape and contraction splits of one contraction.  Estimated time in units of one 64-deep slab of
+// a pair's 256 x 256 tile (about 512 tensor-core cycles): full waves of tiles times slabs, plus a tile's
+// fill and epilogue.  A 128 x 128 tile does a quarter of the work on half the SMs and is bound by its
+// loads (as many bytes per SM as the pair's); a split adds the partial sums' way out and back through
+// memory and one more launch.
 struct LinPlan {
-    int bn, splits, split_slabs;
+    bool pair;
+    int splits, split_slabs;
 };
 LinPlan plan_contraction(long long groups, int rows, int cols, int depth, bool may_split, int sms) {
     const int slabs = (depth + 63) / 64;
-    const long long mt = (rows + 127) / 128;
-    LinPlan best{256, 1, slabs};
+    LinPlan best{false, 1, slabs};
     double best_cost = 1e300;
-    for (int bn = 256; bn >= 128; bn /= 2) {
-        const long long tiles = groups * mt * ((cols + bn - 1) / bn);
+    for (int pair = 1; pair >= 0; --pair) {
+        const int bm = pair ? 256 : 128;
+        const double unit = pair ? 1.0 : 0.6;
+        const int units = pair ? sms / 2 : sms;
+        if (pair && (rows <= 128 || cols <= 128 || units < 1)) continue;
+        const long long tiles = groups * ((rows + bm - 1) / bm) * ((cols + bm - 1) / bm);
         for (int s = 1; s <= (may_split ? 16 : 1); ++s) {
             const int per = (slabs + s - 1) / s;
             if (s > 1 && (per < 4 || (s - 1) * per >= slabs)) continue;
-            const double unit = bn == 256 ? 1.0 : 0.55;
-            const double waves = (double)((tiles * s + sms - 1) / sms);
-            double cost = waves * unit * (per + 3.0);
-            if (s > 1) cost += 20.0 + 8.0 * s * (double)groups * rows * cols / 6.5e12 / 1.4e-7;
+            const double waves = (double)((tiles * s + units - 1) / units);
+            double cost = waves * unit * (per + 2.0);
+            if (s > 1) cost += 10.0 + 8.0 * s * (double)groups * rows * cols / 6.5e12 / 2.8e-7;
             if (cost < best_cost) {
                 best_cost = cost;
-                best = LinPlan{bn, s, per};
+                best = LinPlan{pair != 0, s, per};
             }
         }
     }
@@ -165,9 +180,11 @@ LinParams lin_params(int groups, int rows, int cols, int depth, const LinPlan& p
     p.rows = rows;
     p.cols = cols;
     p.depth = depth;
-    p.mt = (rows + 127) / 128;
-    p.nt = (cols + pl.bn - 1) / pl.bn;
-    p.splits = pl.splits;
+    const int bm = pl.pair ? 256 : 128;
+    p.mt = fast_div((rows + bm - 1) / bm);
+    p.nt = fast_div((cols + bm - 1) / bm);
+    p.splits = fast_div(pl.splits);
+    p.ntile = (int)(groups * p.mt.d * p.nt.d * p.splits.d);
     p.split_slabs = pl.split_slabs;
     return p;
 }
@@ -185,7 +202,7 @@ LinBwdWs carve_lin_bwd(Carve& c, const LinGeo& g, int act) {
     w.dz = act == TM_ACT_NONE ? nullptr : (void*)c.take<uint8_t>((size_t)g.B * cols * g.esz);
     w.chunks = act_bwd_chunks(g.dtype, g.B, cols, g.N, num_sms());
     w.db = c.take<float>((size_t)w.chunks * cols);
-    w.dw_plan = g.dtype == TM_BF16 ? plan_contraction(g.banks, g.N, g.K, g.B, true, num_sms()) : LinPlan{0, 1, 0};
+    w.dw_plan = g.dtype == TM_BF16 ? plan_contraction(g.banks, g.N, g.K, g.B, true, num_sms()) : LinPlan{false, 1, 0};
     w.dw = w.dw_plan.splits > 1 ? c.take<float>((size_t)w.dw_plan.splits * cols * g.K) : nullptr;
     return w;
 }
@@ -249,8 +266,8 @@ tm_status tm_layer_norm(const void* x, const void* residual, tm_layout layout, c
                        {w->gain, g.W * g.esz, false},
                        {w->bias, g.W * g.esz, false},
                        {y, n, true},
-                       {mean_opt, rows * 4, true},
-                       {rstd_opt, rows * 4, true},
+                       {mean_opt, rows * 4, true, 4},
+                       {rstd_opt, rows * 4, true, 4},
                        {save_opt ? save_opt->codes : nullptr, rows * g.W, true},
                        {save_opt ? save_opt->exps : nullptr, ckpt_exps(rows, g.W), true}};
     if (!spans_ok(sp)) return TM_ERR_INVALID_ARG;
@@ -260,7 +277,7 @@ tm_status tm_layer_norm(const void* x, const void* residual, tm_layout layout, c
     p.rstd = rstd_opt;
     p.codes = save_opt ? save_opt->codes : nullptr;
     p.exps = save_opt ? save_opt->exps : nullptr;
-    return cuda_status(launch_ln_fwd(g.dtype, p, (cudaStream_t)stream));
+    return cuda_status(launch_ln_fwd(g.dtype, p, num_sms(), (cudaStream_t)stream));
 }
 
 size_t tm_layer_norm_backward_workspace_bytes(const tm_shape* shape, tm_layout layout, const tm_layer_norm_w* w) {
@@ -293,8 +310,8 @@ tm_status tm_layer_norm_backward(const void* x, const void* residual, const tm_c
                        {saved ? nullptr : residual, n, false},
                        {saved ? saved->codes : nullptr, rows * g.W, false},
                        {saved ? saved->exps : nullptr, ckpt_exps(rows, g.W), false},
-                       {mean, rows * 4, false},
-                       {rstd, rows * 4, false},
+                       {mean, rows * 4, false, 4},
+                       {rstd, rows * 4, false, 4},
                        {dy, n, false},
                        {w->gain, wb, false},
                        {dx, n, true},
@@ -350,20 +367,20 @@ tm_status tm_pertoken_linear(const void* x, const void* residual, const tm_shape
     const LinPlan pl = plan_contraction(g.banks, g.B, g.N, g.K, false, num_sms());
     LinParams p = lin_params(g.banks, g.B, g.N, g.K, pl);
     p.bias = (const __nv_bfloat16*)w->bias;
-    p.add = (const __nv_bfloat16*)residual;
-    p.add_row = (size_t)g.banks * g.N;
-    p.add_group = g.N;
+    p.add = residual != nullptr;
     p.codes = save_opt ? save_opt->codes : nullptr;
     p.exps = save_opt ? save_opt->exps : nullptr;
     p.nblk = (g.N + kCk8Block - 1) / kCk8Block;
-    CUtensorMap ma, mb, mo, mz;
-    if (!map_rows(&ma, x, g.B, g.banks, g.K, 64, 128) || !map_mats(&mb, w->w, g.banks, g.N, g.K, 64, pl.bn) ||
-        !map_rows(&mo, y, g.B, g.banks, g.N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    LinMaps m;
+    if (!map_rows(&m.a, x, g.B, g.banks, g.K, 64, 128) || !map_mats(&m.b, w->w, g.banks, g.N, g.K, 64, 128) ||
+        !map_rows(&m.o, y, g.B, g.banks, g.N, 64, 32))
         return TM_ERR_CUDA;
-    mz = mo;
-    if (z_opt && !map_rows(&mz, z_opt, g.B, g.banks, g.N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return TM_ERR_CUDA;
+    m.r = m.z = m.o;
+    if (residual && !map_rows(&m.r, residual, g.B, g.banks, g.N, 64, 32)) return TM_ERR_CUDA;
+    if (z_opt && !map_rows(&m.z, z_opt, g.B, g.banks, g.N, 64, 32)) return TM_ERR_CUDA;
+    if (save_opt && g.N % 16 == 0 && !map_codes(&m.z, save_opt->codes, g.B, g.banks, g.N)) return TM_ERR_CUDA;
     const int save = z_opt ? LIN_KEEP_FULL : save_opt ? LIN_KEEP_CK8 : LIN_KEEP_NOTHING;
-    return cuda_status(launch_linear_fwd(pl.bn, w->act, save, ma, mb, mo, mz, p, num_sms(), st));
+    return cuda_status(launch_linear_fwd(pl.pair, w->act, save, m, p, num_sms(), st));
 }
 
 size_t tm_pertoken_linear_backward_workspace_bytes(const tm_shape* shape, const tm_linear_w* w) {
@@ -435,27 +452,28 @@ tm_status tm_pertoken_linear_backward(const void* x, const void* dy, const void*
         }
         return TM_OK;
     }
-    CUtensorMap ma, mb, mo;
+    LinMaps m;
     if (dx) {
         const LinPlan pl = plan_contraction(g.banks, g.B, g.K, g.N, false, num_sms());
         LinParams p = lin_params(g.banks, g.B, g.K, g.N, pl);
-        p.add = (const __nv_bfloat16*)dx_add;
-        p.add_row = (size_t)g.banks * g.K;
-        p.add_group = g.K;
-        if (!map_rows(&ma, dz, g.B, g.banks, g.N, 64, 128) || !map_mats(&mb, w->w, g.banks, g.N, g.K, 64, 64) ||
-            !map_rows(&mo, dx, g.B, g.banks, g.K, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+        p.add = dx_add != nullptr;
+        if (!map_rows(&m.a, dz, g.B, g.banks, g.N, 64, 128) || !map_mats(&m.b, w->w, g.banks, g.N, g.K, 64, 64) ||
+            !map_rows(&m.o, dx, g.B, g.banks, g.K, 64, 32))
             return TM_ERR_CUDA;
-        if ((s = cuda_status(launch_linear_dx(pl.bn, ma, mb, mo, p, num_sms(), st))) != TM_OK) return s;
+        m.r = m.z = m.o;
+        if (dx_add && !map_rows(&m.r, dx_add, g.B, g.banks, g.K, 64, 32)) return TM_ERR_CUDA;
+        if ((s = cuda_status(launch_linear_dx(pl.pair, m, p, num_sms(), st))) != TM_OK) return s;
     }
     if (dw) {
         const LinPlan& pl = ws.dw_plan;
         LinParams p = lin_params(g.banks, g.N, g.K, g.B, pl);
-        if (!map_rows(&ma, dz, g.B, g.banks, g.N, 64, 64) || !map_rows(&mb, x, g.B, g.banks, g.K, 64, 64))
+        if (!map_rows(&m.a, dz, g.B, g.banks, g.N, 64, 64) || !map_rows(&m.b, x, g.B, g.banks, g.K, 64, 64))
             return TM_ERR_CUDA;
-        if (pl.splits > 1 ? !map_mats_f32(&mo, ws.dw, (uint64_t)pl.splits * g.banks, g.N, g.K)
-                          : !map_mats(&mo, dw, g.banks, g.N, g.K, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+        if (pl.splits > 1 ? !map_mats_f32(&m.o, ws.dw, (uint64_t)pl.splits * g.banks, g.N, g.K)
+                          : !map_mats(&m.o, dw, g.banks, g.N, g.K, 64, 32))
             return TM_ERR_CUDA;
-        if ((s = cuda_status(launch_linear_dw(pl.bn, ma, mb, mo, p, num_sms(), st))) != TM_OK) return s;
+        m.r = m.z = m.o;
+        if ((s = cuda_status(launch_linear_dw(pl.pair, m, p, num_sms(), st))) != TM_OK) return s;
         if (pl.splits > 1)
             return cuda_status(launch_sum_parts(g.dtype, ws.dw, pl.splits, cols * g.K, dw, st));
     }
