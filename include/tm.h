@@ -468,9 +468,9 @@ TM_API tm_status tm_stack_backward(const void *X, const void *dY, const tm_block
 
 /* 8-bit checkpoint of rows [rows, width].  codes [rows, width] int8; exps [rows, ceil(width / 32)]
  * int8: the 32 values of a block of a row share the scale 2^e, e the smallest integer with
- * max|finite value| <= 127 * 2^e, at least -126 and at most 121; code = nearest integer to value *
- * 2^-e, ties to even, held to +-127 (which only binds above 127 * 2^121); code -128 stands for a value
- * that is not finite and reads back as NaN. */
+ * max|value| <= 127 * 2^e, at least -126 and at most 121; code = nearest integer to value * 2^-e, ties
+ * to even, held to +-127 (which only binds above 127 * 2^121).  A block with a value that is not finite
+ * has e = 127 and codes 0, and reads back as NaN throughout. */
 typedef struct { int8_t *codes; int8_t *exps; } tm_ckpt8;
 
 /* x [rows, width] (dtype f32 or bf16) to a checkpoint, and back (exact in both dtypes).  width >= 1

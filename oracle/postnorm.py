@@ -21,21 +21,23 @@ from scipy.special import erfc, expit
 
 def checkpoint8(z: np.ndarray):
     """(codes, exponents, values) of rows [..., width]: blocks of 32 values share 2^e, e the smallest
-    integer with max|finite| <= 127 * 2^e, at least -126 and at most 121; codes held to +-127; code -128
-    (value NaN) where z is not finite."""
+    integer with max|z| <= 127 * 2^e, at least -126 and at most 121; codes held to +-127.  A block with a
+    value that is not finite has e = 127, codes 0 and values NaN."""
     z = np.asarray(z, np.float64)
     width = z.shape[-1]
     nblk = -(-width // 32)
     b = np.zeros(z.shape[:-1] + (nblk * 32,))
     b[..., :width] = z
     b = b.reshape(z.shape[:-1] + (nblk, 32))
-    fin = np.isfinite(b)
-    top = np.where(fin, np.abs(b), 0.0).max(-1)
+    fin = np.isfinite(b).all(-1)
+    b = np.where(fin[..., None], b, 0.0)
+    top = np.abs(b).max(-1)
     m, x = np.frexp(top)                                   # top = m 2^x, m in [1/2, 1)
     e = np.where(top > 0, x - 7 + (m > 127.0 / 128.0), -126)
     e = np.clip(e, -126, 121)
-    code = np.where(fin, np.clip(np.rint(np.ldexp(np.where(fin, b, 0.0), -e[..., None])), -127, 127), -128)
-    val = np.where(fin, np.ldexp(code, e[..., None]), np.nan)
+    code = np.clip(np.rint(np.ldexp(b, -e[..., None])), -127, 127)
+    val = np.where(fin[..., None], np.ldexp(code, e[..., None]), np.nan)
+    e = np.where(fin, e, 127)
     cut = lambda a: a.reshape(z.shape[:-1] + (nblk * 32,))[..., :width]
     return cut(code).astype(np.int64), e.astype(np.int64), cut(val)
 

@@ -31,8 +31,8 @@ def test_checkpoint_is_the_format_to_the_bit(dtype, rows, width):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("width", [64, 45])
 def test_checkpoint_of_values_at_the_borders(dtype, width):
-    """Infinities and NaN (alone in a block, with others, whole blocks of them), the type's largest and
-    smallest values, zeros, ties, and maxima on both sides of 127 * 2^e."""
+    """Infinities and NaN (alone in a block, with others, whole blocks of them: the block reads back as NaN),
+    the type's largest and smallest values, zeros, ties, and maxima on both sides of 127 * 2^e."""
     fin = torch.finfo(DT[dtype])
     x = torch.zeros(12, width)
     x[0, 3] = float("inf")

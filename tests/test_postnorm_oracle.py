@@ -86,6 +86,6 @@ def test_checkpoint_borders():
     z[0, 0] = np.inf
     z[0, 4] = np.nan
     code, e, val = P.checkpoint8(z)
-    assert e[0, 0] == -5 and code[0, 0] == code[0, 4] == -128 and np.isnan(val[0, [0, 4]]).all() and val[0, 3] == -2.5
+    assert e[0, 0] == 127 and not code.any() and np.isnan(val).all()
     tiny = np.full((1, 5), 2.0 ** -140)
     assert P.checkpoint8(tiny)[1][0, 0] == -126 and not P.checkpoint8(tiny)[0].any()

@@ -12,14 +12,10 @@ namespace tml {
 constexpr int kCk8Threads = 256;
 
 // The vectors of a thread: unit u of a row holds its values u*V .. u*V + V-1; a row has upr units (its
-// last block filled up to 32 / V of them).  A thread's units are a grid's threads apart, so row and
-// unit advance by constants and a carry instead of a division each.
-struct Ck8Walk {
-    long long row;
-    int s;
-};
-
-template <typename T, int V, int U, bool PACK>
+// last block filled up to 32 / V of them).  FLAT: rows are whole blocks, so unit u of the whole tensor
+// is its values u*V .. and block u / (32 / V).  Otherwise a thread's units, which are a grid's threads
+// apart, advance row and unit by constants and a carry instead of a division each.
+template <typename T, int V, int U, bool PACK, bool FLAT>
 __global__ void __launch_bounds__(kCk8Threads)
     ck8_kernel(T* __restrict__ x, int8_t* __restrict__ codes, int8_t* __restrict__ exps, long long rows, int width,
                int nblk) {
@@ -27,39 +23,52 @@ __global__ void __launch_bounds__(kCk8Threads)
     const int upr = nblk * LB;
     const long long total = rows * upr;
     const long long nth = (long long)gridDim.x * blockDim.x;
-    const long long t0 = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    const long long drow = nth / upr;
-    const int ds = (int)(nth - drow * upr);
-    Ck8Walk p{t0 / upr, 0};
-    p.s = (int)(t0 - p.row * upr);
+    long long t0 = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    long long row = 0, drow = 0;
+    int s = 0, ds = 0;
+    if (!FLAT) {
+        drow = nth / upr;
+        ds = (int)(nth - drow * upr);
+        row = t0 / upr;
+        s = (int)(t0 - row * upr);
+    }
     // t0 - lane is the warp's first unit: the loop is uniform across the warp (the shuffles need it)
-    for (long long wu = t0 - (threadIdx.x & 31); wu < total; wu += U * nth) {
-        Ck8Walk at[U];
+    for (; t0 - (threadIdx.x & 31) < total; t0 += U * nth) {
+        long long xo[U], eo[U];
         bool in[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            at[i] = p;
-            in[i] = p.row < rows && p.s * V < width;
-            p.row += drow;
-            p.s += ds;
-            if (p.s >= upr) { p.s -= upr; ++p.row; }
+            if (FLAT) {
+                const long long u = t0 + i * nth;
+                in[i] = u < total;
+                xo[i] = u * V;
+                eo[i] = u / LB;
+            } else {
+                in[i] = row < rows && s * V < width;
+                xo[i] = row * width + s * V;
+                eo[i] = row * nblk + s / LB;
+                row += drow;
+                s += ds;
+                if (s >= upr) { s -= upr; ++row; }
+            }
         }
+        const bool first = threadIdx.x % LB == 0;       // upr and nth are multiples of LB: a block's first lane
         if constexpr (PACK) {
             Pack<T, V> w[U];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                if (in[i]) w[i].load(x + at[i].row * width + at[i].s * V);
+                if (in[i]) w[i].load(x + xo[i]);
                 else w[i].zero();
             }
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                float v[V];
+                float2 v[Pairs<V>::N];
                 w[i].get(v);
                 uint32_t q[(V + 3) / 4];
                 const int e = ck8_quantize<V, LB>(v, q);
                 if (in[i]) {
-                    ck8_store<V>(codes + at[i].row * width + at[i].s * V, q);
-                    if (at[i].s % LB == 0) exps[at[i].row * nblk + at[i].s / LB] = (int8_t)e;
+                    ck8_store<V>(codes + xo[i], q);
+                    if (first) exps[eo[i]] = (int8_t)e;
                 }
             }
         } else {
@@ -67,18 +76,17 @@ __global__ void __launch_bounds__(kCk8Threads)
             int e[U];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                e[i] = 0;
                 if (in[i]) {
-                    ck8_load<V>(codes + at[i].row * width + at[i].s * V, q[i]);
-                    e[i] = __ldg(exps + at[i].row * nblk + at[i].s / LB);
+                    ck8_load<V>(codes + xo[i], q[i]);
+                    e[i] = __ldg(exps + eo[i]);
                 }
             }
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 if (!in[i]) continue;
-                float v[V];
+                float2 v[Pairs<V>::N];
                 ck8_values<V>(q[i], ck8_scale(e[i]), v);
-                Pack<T, V>::store(x + at[i].row * width + at[i].s * V, v);
+                Pack<T, V>::store(x + xo[i], v);
             }
         }
     }
@@ -90,13 +98,15 @@ static cudaError_t launch_ck8_one(void* x, void* codes, void* exps, long long ro
     constexpr int U = 4;
     const int nblk = (width + kCk8Block - 1) / kCk8Block;
     const long long total = rows * nblk * (kCk8Block / V);
-    const long long per = (long long)kCk8Threads * U;
-    long long grid = (total + per - 1) / per;
+    const long long all = (total + kCk8Threads - 1) / kCk8Threads, per = (all + U - 1) / U;
     // small inputs: one unit a thread, so that all SMs take part
-    if (grid < sms) grid = (total + kCk8Threads - 1) / kCk8Threads < sms ? (total + kCk8Threads - 1) / kCk8Threads : sms;
+    long long grid = per > 2LL * sms ? per : (all < 2LL * sms ? all : 2LL * sms);
     if (grid > (1 << 20)) grid = 1 << 20;
     ProfileScope ps_(PACK ? "ckpt8_pack" : "ckpt8_unpack", st);
-    ck8_kernel<T, V, U, PACK><<<(int)grid, kCk8Threads, 0, st>>>((T*)x, (int8_t*)codes, (int8_t*)exps, rows, width, nblk);
+    if (V > 1 && width % kCk8Block == 0)
+        ck8_kernel<T, V, U, PACK, (V > 1)><<<(int)grid, kCk8Threads, 0, st>>>((T*)x, (int8_t*)codes, (int8_t*)exps, rows, width, nblk);
+    else
+        ck8_kernel<T, V, U, PACK, false><<<(int)grid, kCk8Threads, 0, st>>>((T*)x, (int8_t*)codes, (int8_t*)exps, rows, width, nblk);
     return cudaGetLastError();
 }
 

@@ -18,24 +18,47 @@ __device__ __forceinline__ float act_f32(int act, float z) {
     if (act == LIN_SILU) return z / (1.f + expf(-z));
     return z;
 }
-// act'(z): gelu' = Phi(z) + z phi(z); silu' = s (1 + z (1 - s)), s = sigmoid(z)
-template <typename T>
-__device__ __forceinline__ float act_slope(int act, float z) {
-    if (act == LIN_RELU) return z > 0.f ? 1.f : (z == z ? 0.f : z);   // NaN stays
-    if (act == LIN_GELU) {
-        if constexpr (sizeof(T) == 4)
-            return fmaf(z * 0.39894228040143268f, expf(-0.5f * z * z), 0.5f * erfcf(-0.70710678118654752f * z));
-        const float a = fminf(fabsf(z), 16.f);
-        const float q = gauss_tail2(make_float2(a, a)).x;
-        const float cdf = z >= 0.f ? 1.f - q : q;
-        return fmaf(z * 0.39894228040143268f, ex2_approx(-0.72134752044448170f * (z * z)), cdf);
+// act'(z): gelu' = Phi(z) + z phi(z); silu' = s (1 + z (1 - s)), s = sigmoid(z).  ACT is a template
+// parameter of the pass over dy so that its inner loop has no branches.
+template <typename T, int ACT>
+__device__ __forceinline__ float2 act_slope2(float2 z) {
+    if constexpr (ACT == LIN_RELU)            // NaN stays
+        return make_float2(z.x > 0.f ? 1.f : (z.x == z.x ? 0.f : z.x), z.y > 0.f ? 1.f : (z.y == z.y ? 0.f : z.y));
+    if constexpr (ACT == LIN_GELU && sizeof(T) == 4) {
+        auto f = [](float v) {
+            return fmaf(v * 0.39894228040143268f, expf(-0.5f * v * v), 0.5f * erfcf(-0.70710678118654752f * v));
+        };
+        return make_float2(f(z.x), f(z.y));
     }
-    if (act == LIN_SILU) {
-        const float s = sizeof(T) == 4 ? 1.f / (1.f + expf(-z))
-                                       : rcp_approx(1.f + ex2_approx(-1.4426950408889634f * z));
-        return s * fmaf(z, 1.f - s, 1.f);
+    if constexpr (ACT == LIN_SILU && sizeof(T) == 4) {
+        auto f = [](float v) {
+            const float s = 1.f / (1.f + expf(-v));
+            return s * fmaf(v, 1.f - s, 1.f);
+        };
+        return make_float2(f(z.x), f(z.y));
     }
-    return 1.f;
+    if constexpr (ACT == LIN_GELU) {
+        // gelu'(-a) = Q(a) - a phi(a) = 1 - gelu'(a) = exp(-a^2 / 2) U(a), a >= 0, with U(a) = Q(a) / exp(-a^2 / 2)
+        // - a / sqrt(2 pi) as a polynomial of degree 6 (weighted least squares towards the smallest maximum on
+        // [0, 5]): 1.6e-5 off at most, a hundredth of bf16's half step of the slopes it is multiplied into
+        const float2 a = make_float2(fabsf(z.x), fabsf(z.y));
+        const float2 x = mul2(mul2(z, z), f2(-0.72134752044448170f));       // -a^2 / 2 in powers of two
+        float2 u = f2(7.04223057e-4f);
+        u = fma2(u, a, f2(-8.04183446e-3f));
+        u = fma2(u, a, f2(3.96720991e-2f));
+        u = fma2(u, a, f2(-1.16940916e-1f));
+        u = fma2(u, a, f2(2.44423419e-1f));
+        u = fma2(u, a, f2(-7.97151744e-1f));
+        u = fma2(u, a, f2(4.99984294e-1f));
+        const float2 t = mul2(u, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+        return make_float2(z.x < 0.f ? t.x : 1.f - t.x, z.y < 0.f ? t.y : 1.f - t.y);
+    }
+    if constexpr (ACT == LIN_SILU) {
+        const float2 x = mul2(z, f2(-1.4426950408889634f));
+        const float2 s = make_float2(rcp_approx(1.f + ex2_approx(x.x)), rcp_approx(1.f + ex2_approx(x.y)));
+        return mul2(s, fma2(z, fma2(s, f2(-1.f), f2(1.f)), f2(1.f)));
+    }
+    return f2(1.f);
 }
 
 // ------------------------------------------------------------------ dz = dy act'(z), db = sum over b of dz
@@ -43,14 +66,15 @@ __device__ __forceinline__ float act_slope(int act, float z) {
 // rows; the sums over a block's rows go to part [gridDim.y][cols] (in a fixed order).  SRC: what z is
 // read from.  dz may be NULL (no activation: dz is dy, only the sums are wanted).
 enum ZSrc : int { Z_NONE = 0, Z_FULL = 1, Z_CK8 = 2 };
-constexpr int kActX = 64, kActY = 4, kActU = 4;
+constexpr int kActX = 64, kActY = 4;
 
-template <typename T, int V, int SRC>
+template <typename T, int V, int SRC, int ACT>
 __global__ void __launch_bounds__(kActX * kActY)
     act_bwd_kernel(const T* __restrict__ dy, const T* __restrict__ z, const int8_t* __restrict__ codes,
-                   const int8_t* __restrict__ exps, int act, int B, long long cols, int N, int nblk, int rows_per,
+                   const int8_t* __restrict__ exps, int B, long long cols, int N, int nblk, int rows_per,
                    T* __restrict__ dz, float* __restrict__ part) {
-    __shared__ float sm[kActY][kActX][V];
+    constexpr int NP = Pairs<V>::N, U = 4;
+    __shared__ float2 sm[kActY][kActX][NP + 1];          // + 1: rows of a column's pairs in different banks
     const int tx = threadIdx.x % kActX, ty = threadIdx.x / kActX;
     const long long c = ((long long)blockIdx.x * kActX + tx) * V;
     const bool in = c < cols;
@@ -59,16 +83,16 @@ __global__ void __launch_bounds__(kActX * kActY)
     const long long erow = cols / N * nblk;              // exponents per b
     const long long eoff = bank * nblk + n / kCk8Block;
     const int b0 = blockIdx.y * rows_per, b1 = min(B, b0 + rows_per);
-    float s[V];
+    float2 s[NP];
 #pragma unroll
-    for (int k = 0; k < V; ++k) s[k] = 0.f;
+    for (int k = 0; k < NP; ++k) s[k] = make_float2(0.f, 0.f);
     if (in) {
-        for (int b = b0 + ty; b < b1; b += kActY * kActU) {
-            Pack<T, V> dw[kActU], zw[kActU];
-            uint32_t q[kActU][(V + 3) / 4];
-            int e[kActU];
+        for (int b = b0 + ty; b < b1; b += kActY * U) {
+            Pack<T, V> dw[U], zw[SRC == Z_FULL ? U : 1];
+            uint32_t q[SRC == Z_CK8 ? U : 1][(V + 3) / 4];
+            int e[SRC == Z_CK8 ? U : 1];
 #pragma unroll
-            for (int u = 0; u < kActU; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const int r = b + u * kActY;
                 if (r >= b1) continue;
                 dw[u].load(dy + r * cols + c);
@@ -79,34 +103,37 @@ __global__ void __launch_bounds__(kActX * kActY)
                 }
             }
 #pragma unroll
-            for (int u = 0; u < kActU; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const int r = b + u * kActY;
                 if (r >= b1) continue;
-                float d[V], zv[V];
+                float2 d[NP];
                 dw[u].get(d);
                 if constexpr (SRC != Z_NONE) {
+                    float2 zv[NP];
                     if constexpr (SRC == Z_FULL) zw[u].get(zv);
                     else ck8_values<V>(q[u], ck8_scale(e[u]), zv);
 #pragma unroll
-                    for (int k = 0; k < V; ++k) d[k] *= act_slope<T>(act, zv[k]);
+                    for (int k = 0; k < NP; ++k) d[k] = mul2(d[k], act_slope2<T, ACT>(zv[k]));
                     Pack<T, V>::store(dz + r * cols + c, d);
                 }
 #pragma unroll
-                for (int k = 0; k < V; ++k) s[k] += d[k];
+                for (int k = 0; k < NP; ++k) s[k] = add2(s[k], d[k]);
             }
         }
     }
     if (!part) return;
 #pragma unroll
-    for (int k = 0; k < V; ++k) sm[ty][tx][k] = s[k];
+    for (int k = 0; k < NP; ++k) sm[ty][tx][k] = s[k];
     __syncthreads();
     if (ty == 0 && in) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            float t = 0.f;
+        for (int k = 0; k < NP; ++k) {
+            float2 t = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int y = 0; y < kActY; ++y) t += sm[y][tx][k];
-            part[blockIdx.y * cols + c + k] = t;
+            for (int y = 0; y < kActY; ++y) t = add2(t, sm[y][tx][k]);
+            float* o = part + blockIdx.y * cols + c + 2 * k;
+            o[0] = t.x;
+            if (V > 1) o[1] = t.y;
         }
     }
 }
@@ -192,7 +219,8 @@ __global__ void __launch_bounds__(256) linear_simt_kernel(const SimtLin p) {
         const long long r = (long long)m * p.groups + g;      // row of the forward's rows
         if (p.codes) {
             uint32_t q[1];
-            const int e = ck8_quantize<4, 8>(acc[i], q);      // a block of 32 columns: 8 lanes
+            const float2 v2[2] = {make_float2(acc[i][0], acc[i][1]), make_float2(acc[i][2], acc[i][3])};
+            const int e = ck8_quantize<4, 8>(v2, q);          // a block of 32 columns: 8 lanes
             if (row_in) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -303,29 +331,33 @@ int act_bwd_chunks(int dtype, int B, long long cols, int N, int sms) {
 }
 
 template <typename T, int V>
-static void launch_act_bwd_v(int src, const void* dy, const void* z, const int8_t* codes, const int8_t* exps, int act,
-                             int B, long long cols, int N, int chunks, void* dz, float* part, cudaStream_t st) {
+static void launch_act_bwd_v(const void* dy, const void* z, const int8_t* codes, const int8_t* exps, int act, int B,
+                             long long cols, int N, int chunks, void* dz, float* part, cudaStream_t st) {
     const dim3 grid((unsigned)((cols / V + kActX - 1) / kActX), chunks);
     const int per = (B + chunks - 1) / chunks;
     const int nblk = (N + kCk8Block - 1) / kCk8Block;
-#define X(SRC_)                                                                                              \
-    if (src == SRC_)                                                                                         \
-        act_bwd_kernel<T, V, SRC_><<<grid, kActX * kActY, 0, st>>>((const T*)dy, (const T*)z, codes, exps, act, B, \
-                                                                   cols, N, nblk, per, (T*)dz, part);
-    X(Z_NONE) X(Z_FULL) X(Z_CK8)
+#define X(SRC_, ACT_)                                                                                       \
+    act_bwd_kernel<T, V, SRC_, ACT_><<<grid, kActX * kActY, 0, st>>>((const T*)dy, (const T*)z, codes, exps, B, cols, \
+                                                                     N, nblk, per, (T*)dz, part)
+    if (act == LIN_NONE) X(Z_NONE, LIN_NONE);
+    else if (codes && act == LIN_RELU) X(Z_CK8, LIN_RELU);
+    else if (codes && act == LIN_GELU) X(Z_CK8, LIN_GELU);
+    else if (codes) X(Z_CK8, LIN_SILU);
+    else if (act == LIN_RELU) X(Z_FULL, LIN_RELU);
+    else if (act == LIN_GELU) X(Z_FULL, LIN_GELU);
+    else X(Z_FULL, LIN_SILU);
 #undef X
 }
 
 cudaError_t launch_act_bwd(int dtype, const void* dy, const void* z, const int8_t* codes, const int8_t* exps, int act,
                            int B, long long cols, int N, int chunks, void* dz, float* part, cudaStream_t st) {
     ProfileScope ps_("act_bwd", st);
-    const int src = act == LIN_NONE ? Z_NONE : (codes ? Z_CK8 : Z_FULL);
     if (dtype == 1)
-        launch_act_bwd_v<__nv_bfloat16, 8>(src, dy, z, codes, exps, act, B, cols, N, chunks, dz, part, st);
+        launch_act_bwd_v<__nv_bfloat16, 8>(dy, z, codes, exps, act, B, cols, N, chunks, dz, part, st);
     else if (N % 4 == 0)
-        launch_act_bwd_v<float, 4>(src, dy, z, codes, exps, act, B, cols, N, chunks, dz, part, st);
+        launch_act_bwd_v<float, 4>(dy, z, codes, exps, act, B, cols, N, chunks, dz, part, st);
     else
-        launch_act_bwd_v<float, 1>(src, dy, z, codes, exps, act, B, cols, N, chunks, dz, part, st);
+        launch_act_bwd_v<float, 1>(dy, z, codes, exps, act, B, cols, N, chunks, dz, part, st);
     return cudaGetLastError();
 }
 

@@ -30,18 +30,6 @@ enum LinAct : int { LIN_NONE = 0, LIN_RELU = 1, LIN_GELU = 2, LIN_SILU = 3 };
 // what the forward keeps of the pre-activation
 enum LinSave : int { LIN_KEEP_NOTHING = 0, LIN_KEEP_FULL = 1, LIN_KEEP_CK8 = 2 };
 
-// Quotients by a fixed divisor d of 0 <= t < 2^31: (umulhi(m, t) + t) >> l, l = ceil(log2 d),
-// m = floor(2^32 (2^l - d) / d) + 1 (division by an invariant integer through multiplication).
-struct FastDiv {
-    uint32_t d, m, l;
-    __device__ __forceinline__ int div(int t) const { return (int)((__umulhi(m, (uint32_t)t) + (uint32_t)t) >> l); }
-};
-inline FastDiv fast_div(uint32_t d) {
-    uint32_t l = 0;
-    while ((1ull << l) < d) ++l;
-    return FastDiv{d, (uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1), l};
-}
-
 struct LinParams {
     int groups;                // banks
     int rows, cols, depth;     // extents of D and of the contraction, per bank
@@ -424,7 +412,7 @@ __global__ void __launch_bounds__(LinCfg<BN, PAIR, SAVE>::NTHREADS, 1)
                         // this lane's 32 columns are one block of its row (those past the row are zero: their
                         // weights and bias were read as zero); 64 code bytes a row, 64-byte swizzle
                         uint32_t qw[8];
-                        e2[h] = ck8_quantize<32, 1>(v, qw);
+                        e2[h] = ck8_quantize<32, 1>(reinterpret_cast<const float2(&)[16]>(v), qw);
                         if (h == 0) free_box();
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
