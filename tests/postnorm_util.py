@@ -46,11 +46,12 @@ def norm_tols(z, f, gain, bias, dtype):
     g = np.ones(z.shape[-1]) if gain is None else np.abs(gain)
     b = 0.0 if bias is None else np.abs(bias)
     az = np.abs(z).mean(-1)
-    tm = 66 * U * az                                       # the sum, the division, z's own addition (1 u)
+    tm = 67 * U * az                                       # the sum, 1/W and the product with it, z's addition (1 u)
     # d = z - mu is off by tm + 2 u (|z| + |mu|); squares summed (64 u), halved by the root, 4 more steps
     spread = np.abs(z - f["mean"][..., None]).max(-1)
     td = tm + 2 * U * (np.abs(z).max(-1) + np.abs(f["mean"]))
-    tr = f["rstd"] * (70 * U + f["rstd"] * td * 1.01)      # relative: (sum error)/2 + d's error times rstd
+    # relative: half the sum's error, d's error times rstd, and rsqrtf's documented 2 ulp (4 u)
+    tr = f["rstd"] * (70 * U + f["rstd"] * td * 1.01)
     tn = (td * f["rstd"])[..., None] + np.abs(f["n"]) * ((tr / f["rstd"])[..., None] + 4 * U)
     ty = tn * g + 2 * U * (np.abs(f["n"]) * g + b)
     ty = ty + HALF[dtype] * (np.abs(f["y"]) + ty)

@@ -58,7 +58,8 @@ struct NormParams {
     const void* bias;          // NULL: zeros
     RowMap map;                // where x (and dx) lie
     int B;
-    float eps;
+    float eps, inv_w;          // 1 / W
+    FastDiv banks;             // row = b * banks + bank
     // forward
     void* y;
     float* mean;               // [B * banks], forward: may be NULL
@@ -74,9 +75,33 @@ struct NormParams {
 
 template <int G>
 struct NormBlock {
-    static constexpr int THREADS = G > 32 ? G : 256;
+    static constexpr int THREADS = G > 32 ? G : 128;
     static constexpr int ROWS = THREADS / G;
 };
+
+// Where a thread's vectors lie in a row of x: from the row's start in the row layout, from the sample's
+// head piece in the mixed one (column c = t * dh + j at t * D + j).
+template <int V, int NV, int G>
+struct NormCols {
+    int off[NV];
+    __device__ __forceinline__ NormCols(const RowMap& m, int gl) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (gl + G * i) * V;
+            off[i] = c;
+            if (m.layout == 1) {
+                const int t = c / m.dh;
+                off[i] = t * m.D + c - t * m.dh;
+            }
+        }
+    }
+};
+// Start of a row of x (rows <= 2^28).
+__device__ __forceinline__ size_t norm_row(const NormParams& p, int row) {
+    if (p.map.layout == 0) return (size_t)row * p.map.W;
+    const int b = p.banks.div(row);
+    return (size_t)b * p.map.T * p.map.D + (size_t)(row - b * (int)p.banks.d) * p.map.dh;
+}
 
 // A vector of gain or bias [W] in shared memory as fp32.  V = 8: the two halves of each vector apart, so
 // that neighbouring lanes read neighbouring 16 bytes.
@@ -105,7 +130,7 @@ __device__ __forceinline__ void staged(const float* s, int W, int c, float2 (&v)
 
 // A row's statistics, checkpoint and output from its z in registers (zeros past the row).
 template <typename T, int V, int NV, int G>
-__device__ __forceinline__ void ln_fwd_row(const NormParams& p, float2 (&z)[NV][Pairs<V>::N], bool live, long long row,
+__device__ __forceinline__ void ln_fwd_row(const NormParams& p, float2 (&z)[NV][Pairs<V>::N], bool live, int row,
                                            int gl, const float* sg, const float* sb, float2* red, int& turn) {
     constexpr int NP = Pairs<V>::N;
     const int W = p.map.W;
@@ -115,7 +140,7 @@ __device__ __forceinline__ void ln_fwd_row(const NormParams& p, float2 (&z)[NV][
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int k = 0; k < NP; ++k) s2 = add2(s2, z[i][k]);
-    const float mu = row_sum<G>(s2.x + s2.y, red, turn) / (float)W;
+    const float mu = row_sum<G>(s2.x + s2.y, red, turn) * p.inv_w;
     if (p.codes) {
         constexpr int LB = kCk8Block / V;
         const int nblk = (W + kCk8Block - 1) / kCk8Block;
@@ -126,7 +151,7 @@ __device__ __forceinline__ void ln_fwd_row(const NormParams& p, float2 (&z)[NV][
             const int e = ck8_quantize<V, LB>(z[i], q);
             if (live && c < W) {
                 ck8_store<V>(p.codes + ro + c, q);
-                if (c % kCk8Block == 0) p.exps[row * nblk + c / kCk8Block] = (int8_t)e;
+                if (c % kCk8Block == 0) p.exps[(size_t)row * nblk + c / kCk8Block] = (int8_t)e;
             }
         }
     }
@@ -143,7 +168,7 @@ __device__ __forceinline__ void ln_fwd_row(const NormParams& p, float2 (&z)[NV][
             }
         }
     }
-    const float rs = 1.0f / sqrtf(row_sum<G>(s2.x + s2.y, red, turn) / (float)W + p.eps);
+    const float rs = rsqrtf(row_sum<G>(s2.x + s2.y, red, turn) * p.inv_w + p.eps);
     if (!live) return;
     if (gl == 0) {
         if (p.mean) p.mean[row] = mu;
@@ -172,25 +197,25 @@ __global__ void __launch_bounds__(NormBlock<G>::THREADS) ln_fwd_kernel(const Nor
     int turn = 0;
     const int W = p.map.W;
     const int gl = threadIdx.x % G;
-    const long long nrows = (long long)p.B * p.map.banks;
-    const long long step = (long long)gridDim.x * ROWS;
+    const int nrows = p.B * p.map.banks;
+    const int step = gridDim.x * ROWS;
+    const NormCols<V, NV, G> cols(p.map, gl);
     Pack<T, V> xw[NV], rw[NV];
-    auto load = [&](long long row) {
+    auto load = [&](int row) {
         const bool live = row < nrows;      // lanes past the last row take part in the shuffles, on zeros
-        const int b = live ? (int)(row / p.map.banks) : 0;
-        const int bank = live ? (int)(row - (long long)b * p.map.banks) : 0;
+        const T* x = (const T*)p.x + norm_row(p, live ? row : 0);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (gl + G * i) * V;
             xw[i].zero();
             rw[i].zero();
             if (live && c < W) {
-                xw[i].load((const T*)p.x + row_elem(p.map, b, bank, c));
+                xw[i].load(x + cols.off[i]);
                 if (p.res) rw[i].load((const T*)p.res + (size_t)row * W + c);
             }
         }
     };
-    long long base = (long long)blockIdx.x * ROWS;
+    int base = blockIdx.x * ROWS;
     load(base + threadIdx.x / G);
     float *sg = nsm, *sb = nsm + W;
     stage_vec<T, V>(sg, p.gain, W, 1.f);
@@ -206,7 +231,7 @@ __global__ void __launch_bounds__(NormBlock<G>::THREADS) ln_fwd_kernel(const Nor
 #pragma unroll
             for (int k = 0; k < NP; ++k) z[i][k] = add2(z[i][k], r[k]);
         }
-        const long long row = base + threadIdx.x / G;
+        const int row = base + threadIdx.x / G;
         if (base + step < nrows) load(row + step);
         const bool live = row < nrows;
         ln_fwd_row<T, V, NV, G>(p, z, live, live ? row : 0, gl, sg, sb, red, turn);
@@ -223,9 +248,10 @@ struct NormRow {
     int e[CK ? NV : 1];
 
     template <int G>
-    __device__ __forceinline__ void load(const NormParams& p, bool live, long long row, int b, int bank, int gl) {
+    __device__ __forceinline__ void load(const NormParams& p, bool live, int row, const NormCols<V, NV, G>& cols, int gl) {
         const int W = p.map.W;
         const size_t ro = (size_t)row * W;
+        const T* x = CK ? nullptr : (const T*)p.x + norm_row(p, row);
         const int nblk = (W + kCk8Block - 1) / kCk8Block;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -243,9 +269,9 @@ struct NormRow {
                 dw[i].load((const T*)p.dy + ro + c);
                 if constexpr (CK) {
                     ck8_load<V>(p.codes + ro + c, q[i]);
-                    e[i] = __ldg(p.exps + row * nblk + c / kCk8Block);
+                    e[i] = __ldg(p.exps + (size_t)row * nblk + c / kCk8Block);
                 } else {
-                    xw[i].load((const T*)p.x + row_elem(p.map, b, bank, c));
+                    xw[i].load(x + cols.off[i]);
                     if (p.res) rw[i].load((const T*)p.res + ro + c);
                 }
             }
@@ -305,7 +331,7 @@ __device__ __forceinline__ void ln_bwd_row(const NormParams& p, const NormRow<T,
         }
     }
     const float2 m = row_sum2<G>(make_float2(s1.x + s1.y, s2.x + s2.y), red, turn);
-    const float2 m1 = f2(-rs * (m.x / (float)W)), m2 = f2(-rs * (m.y / (float)W));
+    const float2 m1 = f2(-rs * (m.x * p.inv_w)), m2 = f2(-rs * (m.y * p.inv_w));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (gl + G * i) * V, a = KEEP ? i : 0;
@@ -314,7 +340,7 @@ __device__ __forceinline__ void ln_bwd_row(const NormParams& p, const NormRow<T,
             if (!KEEP) make(i, c, n[a], dn[a], d);
 #pragma unroll
             for (int k = 0; k < NP; ++k) d[k] = fma2(dn[a][k], f2(rs), fma2(n[a][k], m2, m1));
-            emit(c, d);
+            emit(i, c, d);
         }
     }
 }
@@ -376,41 +402,40 @@ __global__ void __launch_bounds__(NormBlock<G>::THREADS) ln_bwd_kernel(const Nor
     int turn = 0;
     const int W = p.map.W;
     const int gl = threadIdx.x % G;
-    const long long nrows = (long long)p.B * p.map.banks;
+    const int nrows = p.B * p.map.banks;
     const bool mixed = p.map.layout == 1;
+    const NormCols<V, NV, G> cols(p.map, gl);
     float2 dg[NV][NP], db[NV][NP];
     zero_sums<V, NV>(dg, db);
     struct At {
-        long long row;
-        bool live;
-        int b, bank;
+        int row;                            // < 0: a group without a row, on zeros, which add nothing
         float mu, rs;
     };
     NormRow<T, V, NV, CK> rn;
-    auto fetch = [&](long long base) -> At {
+    auto fetch = [&](int base) -> At {
         At a;
-        a.row = base + threadIdx.x / G;
-        a.live = a.row < nrows;             // a group without a row works on zeros, which add nothing
-        a.b = a.live ? (int)(a.row / p.map.banks) : 0;
-        a.bank = a.live ? (int)(a.row - (long long)a.b * p.map.banks) : 0;
-        a.mu = a.live ? __ldg(p.mean + a.row) : 0.f;
-        a.rs = a.live ? __ldg(p.rstd + a.row) : 0.f;
-        rn.template load<G>(p, a.live, a.row, a.b, a.bank, gl);
+        const int row = base + threadIdx.x / G;
+        const bool live = row < nrows;
+        a.row = live ? row : -1;
+        a.mu = live ? __ldg(p.mean + row) : 0.f;
+        a.rs = live ? __ldg(p.rstd + row) : 0.f;
+        rn.template load<G>(p, live, live ? row : 0, cols, gl);
         return a;
     };
-    const long long step = (long long)gridDim.x * ROWS;
-    long long base = (long long)blockIdx.x * ROWS;
+    const int step = gridDim.x * ROWS;
+    int base = blockIdx.x * ROWS;
     At an = fetch(base);
     stage_vec<T, V>(nsm, p.gain, W, 1.f);
     __syncthreads();
     for (; base < nrows; base += step) {
-        if (!AHEAD && base != (long long)blockIdx.x * ROWS) an = fetch(base);
+        if (!AHEAD && base != (int)blockIdx.x * ROWS) an = fetch(base);
         const NormRow<T, V, NV, CK> r = rn;
         const At a = an;
         if (AHEAD && base + step < nrows) an = fetch(base + step);
-        ln_bwd_row<T, V, NV, G, CK>(p, r, a.mu, a.rs, gl, nsm, red, turn, dg, db, [&](int c, const float2(&d)[NP]) {
-            if (!a.live) return;
-            Pack<T, V>::store((T*)p.dx + row_elem(p.map, a.b, a.bank, c), d);
+        T* dx = (T*)p.dx + norm_row(p, max(a.row, 0));
+        ln_bwd_row<T, V, NV, G, CK>(p, r, a.mu, a.rs, gl, nsm, red, turn, dg, db, [&](int i, int c, const float2(&d)[NP]) {
+            if (a.row < 0) return;
+            Pack<T, V>::store(dx + cols.off[i], d);
             if (mixed && p.dres) Pack<T, V>::store((T*)p.dres + (size_t)a.row * W + c, d);
         });
     }
@@ -431,15 +456,16 @@ __global__ void __launch_bounds__(THREADS) ln_bwd_self_kernel(const NormParams p
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     stage_vec<T, V>(nsm, p.gain, W, 1.f);
     __syncthreads();
+    const NormCols<V, NV, 32> cols(p.map, lane);
     float2 dg[NV][NP], db[NV][NP];
     zero_sums<V, NV>(dg, db);
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         for (int h = warp; h < H; h += THREADS / 32) {
-            const long long row = (long long)b * H + h;
+            const int row = b * H + h;
             NormRow<T, V, NV, CK> r;
             const float mu = __ldg(p.mean + row), rs = __ldg(p.rstd + row);
-            r.template load<32>(p, true, row, b, h, lane);
-            ln_bwd_row<T, V, NV, 32, CK>(p, r, mu, rs, lane, nsm, nullptr, turn, dg, db, [&](int c, const float2(&d)[NP]) {
+            r.template load<32>(p, true, row, cols, lane);
+            ln_bwd_row<T, V, NV, 32, CK>(p, r, mu, rs, lane, nsm, nullptr, turn, dg, db, [&](int, int c, const float2(&d)[NP]) {
 #pragma unroll
                 for (int k = 0; k < NP; k += 2)
                     *reinterpret_cast<float4*>(sm + (size_t)h * W + c + 2 * k) = make_float4(d[k].x, d[k].y, d[k + 1].x, d[k + 1].y);
@@ -503,7 +529,10 @@ __global__ void __launch_bounds__(THREADS) ln_sample_fwd_kernel(const NormParams
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int turn = 0;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < nb; ++i) mbar_init(&bars[i], 1);
+        for (int i = 0; i < nb; ++i) {
+            mbar_init(&bars[i], 1);
+            mbar_init(&bars[4 + i], THREADS / 32);
+        }
         fence_barrier_init();
     }
     __syncthreads();
@@ -523,14 +552,16 @@ __global__ void __launch_bounds__(THREADS) ln_sample_fwd_kernel(const NormParams
         const int c = (lane + 32 * i) * V, t = c / dh;
         moff[i] = t * (int)ld + (c - t * dh) * ES;
     }
+    __syncthreads();
+    // Warps go from sample to sample on their own: a slot is loaded again when every warp has arrived on
+    // its second barrier.
     int slot = 0;
     uint32_t ph = 0;
     int done = 0;
     for (; done < mine; ++done) {
-        const bool ok = mbar_wait(&bars[slot], ph, 0x810);
-        if (!__syncthreads_and(ok)) break;
+        if (!mbar_wait(&bars[slot], ph, 0x810)) break;
         const uint8_t* sx = sms + slot * ring.slot_bytes;
-        const long long b = blockIdx.x + (long long)done * gridDim.x;
+        const int b = blockIdx.x + done * gridDim.x;
         for (int h = warp; h < H; h += THREADS / 32) {
             float2 z[NV][NP];
 #pragma unroll
@@ -551,12 +582,15 @@ __global__ void __launch_bounds__(THREADS) ln_sample_fwd_kernel(const NormParams
             }
             ln_fwd_row<T, V, NV, 32>(p, z, true, b * H + h, lane, sg, sb, nullptr, turn);
         }
-        __syncthreads();
-        if (warp == 0 && done + nb < mine)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[4 + slot]);
+        if (warp == 0 && done + nb < mine) {
+            if (!mbar_wait(&bars[4 + slot], ph, 0x815)) break;
             sample_load(ring, slot, x + (b + (size_t)nb * gridDim.x) * per, H, bytes, ld);
+        }
         if (++slot == nb) { slot = 0; ph ^= 1; }
     }
-    if (done < mine && threadIdx.x == 0)    // given up: the loads in flight land before the block ends
+    if (done < mine && warp == 0)           // given up: the loads in flight land before the block ends
         for (int i = 0; i < nb && done + i < mine; ++i) {
             mbar_wait(&bars[slot], ph, 0x811);
             if (++slot == nb) { slot = 0; ph ^= 1; }
@@ -661,7 +695,7 @@ __global__ void __launch_bounds__(THREADS)
                 }
             }
             const float2 m = row_sum2<32>(make_float2(s1.x + s1.y, s2.x + s2.y), nullptr, turn);
-            if (lane == 0) rowc[h] = make_float4(rs, mu, -rs * (m.x / (float)W), -rs * rs * (m.y / (float)W));
+            if (lane == 0) rowc[h] = make_float4(rs, mu, -rs * (m.x * p.inv_w), -rs * rs * (m.y * p.inv_w));
         }
         __syncthreads();
         // pairs (t <= h): rows i and H-1-i of the triangle together are H + 1 pieces
@@ -757,7 +791,7 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const float* __restric
 // ------------------------------------------------------------------ launchers
 // Rows of W columns in vectors of V: vectors per thread NV and threads per row G, the first that holds W.
 #define TM_NORM_BF16(X) \
-    X(8, 1, 8) X(8, 1, 16) X(8, 1, 32) X(4, 3, 32) X(8, 2, 32) X(8, 3, 32) X(8, 4, 32) X(8, 2, 128) X(8, 4, 128) X(8, 4, 512)
+    X(8, 1, 8) X(8, 1, 16) X(8, 1, 32) X(8, 3, 16) X(8, 2, 32) X(8, 3, 32) X(8, 4, 32) X(8, 2, 128) X(8, 4, 128) X(8, 4, 512)
 #define TM_NORM_F32(X) \
     X(4, 1, 8) X(4, 1, 16) X(4, 1, 32) X(4, 2, 32) X(4, 3, 32) X(4, 4, 32) X(4, 8, 32) X(4, 4, 128) X(4, 8, 128) X(4, 8, 512)
 #define TM_NORM_ODD(X) X(1, 4, 32) X(1, 16, 32) X(1, 16, 128) X(1, 32, 512)

@@ -60,6 +60,8 @@ NormParams norm_params(const Geo& g, const tm_layer_norm_w* w, const void* x, co
     p.map = g.map;
     p.B = g.B;
     p.eps = g.eps;
+    p.inv_w = 1.0f / (float)g.W;
+    p.banks = fast_div(g.banks);
     return p;
 }
 
