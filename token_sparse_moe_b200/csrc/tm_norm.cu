@@ -353,11 +353,12 @@ __device__ __forceinline__ void zero_sums(float2 (&dg)[NV][Pairs<V>::N], float2 
         for (int k = 0; k < Pairs<V>::N; ++k) dg[i][k] = db[i][k] = make_float2(0.f, 0.f);
 }
 
-// The block's sums of dgain and dbias over its row groups (group r's thread gl holds columns (gl + G i) V ..),
-// in a fixed order: through shared memory, one of the two at a time and `room` groups at a time; sm holds
-// room * W floats and is free when this is called.
+// The block's sums of dgain and dbias over its row groups (group grp's thread gl holds columns c0 + (gl + G i) V
+// .. below c1), in a fixed order: through shared memory, one of the two at a time and `room` groups at a
+// time; sm holds room * W floats and is free when this is called.
 template <int V, int NV, int G>
 __device__ __forceinline__ void ln_store_partials(const NormParams& p, float* sm, int room, int groups, int grp, int gl,
+                                                  int c0, int c1,
                                                   const float2 (&dg)[NV][Pairs<V>::N],
                                                   const float2 (&db)[NV][Pairs<V>::N]) {
     const int W = p.map.W;
@@ -368,8 +369,8 @@ __device__ __forceinline__ void ln_store_partials(const NormParams& p, float* sm
             if (grp >= g0 && grp < g0 + room) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int c = (gl + G * i) * V;
-                    if (c < W) {
+                    const int c = c0 + (gl + G * i) * V;
+                    if (c < c1) {
                         float* o = sm + (grp - g0) * W + c;
 #pragma unroll
                         for (int k = 0; k < Pairs<V>::N; ++k) {
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(NormBlock<G>::THREADS) ln_bwd_kernel(const Nor
             if (mixed && p.dres) Pack<T, V>::store((T*)p.dres + (size_t)a.row * W + c, d);
         });
     }
-    if (p.part) ln_store_partials<V, NV, G>(p, nsm + W, ROWS, ROWS, threadIdx.x / G, gl, dg, db);
+    if (p.part) ln_store_partials<V, NV, G>(p, nsm + W, ROWS, ROWS, threadIdx.x / G, gl, 0, W, dg, db);
 }
 
 // Backward of LN(Mix(X) + X) (T = H, W = D) for samples that the ring of ln_sample_bwd_kernel does not take:
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(THREADS) ln_bwd_self_kernel(const NormParams p
         }
         __syncthreads();
     }
-    if (p.part) ln_store_partials<V, NV, 32>(p, sm, min(H, THREADS / 32), THREADS / 32, warp, lane, dg, db);
+    if (p.part) ln_store_partials<V, NV, 32>(p, sm, min(H, THREADS / 32), THREADS / 32, warp, lane, 0, W, dg, db);
 }
 
 // ------------------------------------------------------------------ whole samples: LN(Mix(X) + X)
@@ -515,11 +516,26 @@ __device__ __forceinline__ void sample_load(const SampleRing& r, int slot, const
     for (int t = lane; t < rows; t += 32) bulk_load(dst + t * ld, (const uint8_t*)src + (size_t)t * bytes, bytes, bar);
 }
 
+// Waits for a phase by one lane of the warp; then every lane sees for itself that it is complete.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned where) {
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, where);
+    ok = __all_sync(0xffffffffu, ok);
+    mbar_try_wait(bar, parity);
+    return ok;
+}
+
+// Working warps of the sample kernels, beside the one that loads (issuing a sample's 48 row copies takes
+// a warp some 4000 cycles): rows of up to 64 vectors leave room for several blocks an SM, whose loads,
+// arithmetic and stores then overlap; wider rows come in samples that fill an SM.
+constexpr int sample_warps(int nv) { return nv <= 2 ? 8 : 24; }
+
 // Dynamic shared memory: nb slots, then gain and bias.
-template <typename T, int V, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS) ln_sample_fwd_kernel(const NormParams p, uint32_t ld, int nb) {
+template <typename T, int V, int NV, int NW>
+__global__ void __launch_bounds__(NW * 32 + 32, NV <= 2 ? 3 : 1)
+    ln_sample_fwd_kernel(const NormParams p, uint32_t ld, int nb) {
     extern __shared__ __align__(128) uint8_t sms[];
-    __shared__ uint64_t bars[8];
+    __shared__ uint64_t bars[8];               // [slot] loaded, [4 + slot] read by every warp
     constexpr int NP = Pairs<V>::N, ES = sizeof(T);
     const int W = p.map.W, H = p.map.banks, dh = p.map.dh;
     const uint32_t bytes = W * ES;
@@ -531,18 +547,39 @@ __global__ void __launch_bounds__(THREADS) ln_sample_fwd_kernel(const NormParams
     if (threadIdx.x == 0) {
         for (int i = 0; i < nb; ++i) {
             mbar_init(&bars[i], 1);
-            mbar_init(&bars[4 + i], THREADS / 32);
+            mbar_init(&bars[4 + i], NW);
         }
         fence_barrier_init();
     }
     __syncthreads();
-    const T* x = (const T*)p.x;
     const size_t per = (size_t)H * W;
-    // load i of this block is sample blockIdx.x + i * gridDim.x, in slot i % nb
+    // sample i of this block is blockIdx.x + i * gridDim.x, in slot i % nb
     const int mine = blockIdx.x < p.B ? (p.B - 1 - blockIdx.x) / gridDim.x + 1 : 0;
-    if (warp == 0)
-        for (int i = 0; i < nb && i < mine; ++i)
-            sample_load(ring, i, x + (blockIdx.x + (size_t)i * gridDim.x) * per, H, bytes, ld);
+    if (warp == NW) {
+        int slot = 0, i = 0;
+        uint32_t ph = 0;
+        for (; i < mine; ++i) {
+            if (i >= nb && !warp_wait(&bars[4 + slot], ph ^ 1, 0x815)) break;
+            sample_load(ring, slot, (const T*)p.x + (blockIdx.x + (size_t)i * gridDim.x) * per, H, bytes, ld);
+            if (++slot == nb) { slot = 0; ph ^= 1; }
+            if (i == 0) break;                 // the first on its way, then the vectors of all rows
+        }
+        stage_vec<T, V>(sg, p.gain, W, 1.f);
+        stage_vec<T, V>(sb, p.bias, W, 0.f);
+        __syncthreads();
+        for (++i; i < mine; ++i) {
+            if (i >= nb && !warp_wait(&bars[4 + slot], ph ^ 1, 0x815)) break;
+            sample_load(ring, slot, (const T*)p.x + (blockIdx.x + (size_t)i * gridDim.x) * per, H, bytes, ld);
+            if (++slot == nb) { slot = 0; ph ^= 1; }
+        }
+        if (i < mine)                          // given up: the loads in flight land before the block ends
+            for (int k = 0; k < nb && k < i; ++k) {
+                if (slot == 0) { slot = nb; ph ^= 1; }
+                --slot;
+                mbar_wait(&bars[slot], ph, 0x811);
+            }
+        return;
+    }
     stage_vec<T, V>(sg, p.gain, W, 1.f);
     stage_vec<T, V>(sb, p.bias, W, 0.f);
     // byte offsets of the Mix view's pieces that this lane's vectors are
@@ -553,16 +590,14 @@ __global__ void __launch_bounds__(THREADS) ln_sample_fwd_kernel(const NormParams
         moff[i] = t * (int)ld + (c - t * dh) * ES;
     }
     __syncthreads();
-    // Warps go from sample to sample on their own: a slot is loaded again when every warp has arrived on
-    // its second barrier.
+    // warps go from sample to sample on their own
     int slot = 0;
     uint32_t ph = 0;
-    int done = 0;
-    for (; done < mine; ++done) {
-        if (!mbar_wait(&bars[slot], ph, 0x810)) break;
+    for (int done = 0; done < mine; ++done) {
+        if (!warp_wait(&bars[slot], ph, 0x810)) break;
         const uint8_t* sx = sms + slot * ring.slot_bytes;
         const int b = blockIdx.x + done * gridDim.x;
-        for (int h = warp; h < H; h += THREADS / 32) {
+        for (int h = warp; h < H; h += NW) {
             float2 z[NV][NP];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -584,108 +619,134 @@ __global__ void __launch_bounds__(THREADS) ln_sample_fwd_kernel(const NormParams
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[4 + slot]);
-        if (warp == 0 && done + nb < mine) {
-            if (!mbar_wait(&bars[4 + slot], ph, 0x815)) break;
-            sample_load(ring, slot, x + (b + (size_t)nb * gridDim.x) * per, H, bytes, ld);
-        }
         if (++slot == nb) { slot = 0; ph ^= 1; }
     }
-    if (done < mine && warp == 0)           // given up: the loads in flight land before the block ends
-        for (int i = 0; i < nb && done + i < mine; ++i) {
-            mbar_wait(&bars[slot], ph, 0x811);
-            if (++slot == nb) { slot = 0; ph ^= 1; }
-        }
 }
 
 // Backward of the same, dX = dz + Revert(dz).  Mix(X) + X is symmetric under exchange of a token and a
 // head (its element (row h, column t * dh + j) is X[t][h * dh + j] + X[h][t * dh + j]), and so is dX:
-// dX[t][h * dh + j] = dz[t][h * dh + j] + dz[h][t * dh + j] = dX[h][t * dh + j].  A sample takes two
-// slots (X or the checkpoint's codes, and dy).  First its rows' two means, with dgain and dbias on the
-// way, a warp a row; then every pair of elements once, from the same shared memory: dz is never stored.
-// Dynamic shared memory: nb slots, gain, [H] row constants.
-template <typename T, int V, int NV, bool CK, int THREADS>
-__global__ void __launch_bounds__(THREADS)
-    ln_sample_bwd_kernel(const NormParams p, uint32_t ld, uint32_t ldc, int nb, FastDiv vpd, FastDiv hp1) {
+// dX[t][h * dh + j] = dz[t][h * dh + j] + dz[h][t * dh + j] = dX[h][t * dh + j].  First a sample's row
+// means, with dgain and dbias on the way, a warp a row (or one of PARTS parts of it, so that the sums fit
+// the registers of 24 warps); then every pair of elements once: dz is never stored.  Three slots: X (or the
+// checkpoint's codes) of this sample and of the next, and dy.  The second step reads dy again through the
+// L2, where the first's copy has just come from, so that the next dy is on its way meanwhile: with dy kept
+// in its slot to the end, two samples of 73 KB do not fit, and a third of the time went by waiting for the
+// next one.  Every warp issues some of a sample's row copies (all of them take one warp some 4000 cycles).
+// VA: vector of the first step (parts of W / PARTS columns), NVA of them a lane.
+// Dynamic shared memory: 3 slots, gain, [H] row constants, [H] statistics, [PARTS][H] sums.
+template <typename T, int VA, int NVA, int PARTS, bool CK, int NW>
+__global__ void __launch_bounds__(NW * 32, NW <= 8 ? 2 : 1)
+    ln_sample_bwd_kernel(const NormParams p, uint32_t ld, uint32_t ldc) {
     extern __shared__ __align__(128) uint8_t sms[];
-    __shared__ uint64_t bars[8];
-    constexpr int NW = THREADS / 32, NP = Pairs<V>::N, ES = sizeof(T);
+    __shared__ uint64_t bars[3];       // loaded: X slots 0 and 1, dy
+    constexpr int V = sizeof(T) == 2 ? 8 : 4, NP = Pairs<V>::N, NPA = Pairs<VA>::N, ES = sizeof(T);
     const int W = p.map.W, H = p.map.banks, dh = p.map.dh;
     const int nblk = (W + kCk8Block - 1) / kCk8Block;
     const uint32_t bytes = W * ES;
-    const SampleRing ring{sms, bars, H * ld, nb};
-    float* sg = reinterpret_cast<float*>(sms + (size_t)nb * ring.slot_bytes);
-    float4* rowc = reinterpret_cast<float4*>(sg + W);      // [H] {rs, mu, -rs m1, -rs^2 m2}
+    const SampleRing ring{sms, bars, H * ld, 3};
+    float* sg = reinterpret_cast<float*>(sms + (size_t)3 * ring.slot_bytes);
+    float4* rowc = reinterpret_cast<float4*>(sg + W);      // {rs, mu, -rs m1, -rs^2 m2}
+    float2* rowstat = reinterpret_cast<float2*>(rowc + H); // {mu, rs}
+    float2* rowsum = rowstat + H;                          // [PARTS][H] sums of dn and dn n
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int turn = 0;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < nb; ++i) mbar_init(&bars[i], 1);
+        for (int i = 0; i < 3; ++i) mbar_init(&bars[i], 1);
         fence_barrier_init();
     }
     __syncthreads();
     const size_t per = (size_t)H * W;
     const int mine = blockIdx.x < p.B ? (p.B - 1 - blockIdx.x) / gridDim.x + 1 : 0;
-    // load 2 i is sample i's X (or codes), load 2 i + 1 its dy; load l goes to slot l % nb
-    auto load = [&](int l, int slot) {
-        const size_t b = blockIdx.x + (size_t)(l >> 1) * gridDim.x;
-        if (l & 1) sample_load(ring, slot, (const T*)p.dy + b * per, H, bytes, ld);
-        else if (CK) sample_load(ring, slot, p.codes + b * per, H, W, ldc);
-        else sample_load(ring, slot, (const T*)p.x + b * per, H, bytes, ld);
+    float2 dg[NVA][NPA], db[NVA][NPA];
+    zero_sums<VA, NVA>(dg, db);
+    const int part = warp % PARTS, c0 = part * (W / PARTS), c1 = c0 + W / PARTS;
+    // this block's i-th sample, row copies dealt out to the warps: X or codes into slot i % 2, dy into slot 2
+    auto load = [&](int slot, const void* src, uint32_t row_bytes, uint32_t row_ld) {
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(&bars[slot], H * row_bytes);
+        uint8_t* dst = sms + slot * ring.slot_bytes;
+        for (int t = lane * NW + warp; t < H; t += 32 * NW)
+            bulk_load(dst + t * row_ld, (const uint8_t*)src + (size_t)t * row_bytes, row_bytes, &bars[slot]);
     };
-    if (warp == 0)
-        for (int l = 0; l < nb && l < 2 * mine; ++l) load(l, l);
+    auto load_x = [&](int i) {
+        const size_t b = blockIdx.x + (size_t)i * gridDim.x;
+        if (CK) load(i & 1, p.codes + b * per, W, ldc);
+        else load(i & 1, (const T*)p.x + b * per, bytes, ld);
+    };
+    auto load_d = [&](int i) { load(2, (const T*)p.dy + (blockIdx.x + (size_t)i * gridDim.x) * per, bytes, ld); };
+    if (mine > 0) {
+        load_x(0);
+        load_d(0);
+    }
     stage_vec<T, V>(sg, p.gain, W, 1.f);
-    float2 dg[NV][NP], db[NV][NP];
-    zero_sums<V, NV>(dg, db);
-    int moff[NV];
+    int moff[NVA];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (lane + 32 * i) * V, t = c / dh;
+    for (int i = 0; i < NVA; ++i) {
+        const int c = c0 + (lane + 32 * i) * VA, t = c / dh;
         moff[i] = t * (int)ld + (c - t * dh) * ES;
     }
-    const int npair = (H + 1) / 2 * (H + 1) * (int)vpd.d;  // vpd: vectors of a piece
-    int slot = 0;
-    uint32_t ph = 0;
+    // the second step's vectors: (H + 1) / 2 folded rows of H + 1 pieces of vpd vectors; this thread's
+    // first and the step to its next
+    constexpr int TH = NW * 32;
+    const int vpd = dh / V, npair = (H + 1) / 2 * (H + 1) * vpd;
+    const int j0 = threadIdx.x % vpd, k0 = threadIdx.x / vpd % (H + 1), i0 = threadIdx.x / vpd / (H + 1);
+    const int dj = TH % vpd, dk = TH / vpd % (H + 1), di = TH / vpd / (H + 1);
+    // thread h < H holds row h's statistics a sample ahead (H <= 256 = the smallest block: W >= 4 H)
+    float2 stat = make_float2(0.f, 0.f);
+    auto fetch_stat = [&](int b) {
+        if (threadIdx.x < H)
+            stat = make_float2(__ldg(p.mean + (size_t)b * H + threadIdx.x), __ldg(p.rstd + (size_t)b * H + threadIdx.x));
+    };
+    if (mine > 0) fetch_stat(blockIdx.x);
+    __syncthreads();
     int done = 0;
     for (; done < mine; ++done) {
-        const int slot2 = slot + 1 == nb ? 0 : slot + 1;
-        const bool ok = mbar_wait(&bars[slot], ph, 0x812) && mbar_wait(&bars[slot2], slot2 ? ph : ph ^ 1, 0x813);
+        const uint32_t phx = (done >> 1) & 1, phd = done & 1;
+        // one warp waits for the data, the others at the barrier; it also says that every warp is done with
+        // the last sample, its slot of X and its row constants
+        const bool ok = warp != 0 || (warp_wait(&bars[done & 1], phx, 0x812) && warp_wait(&bars[2], phd, 0x813));
+        if (threadIdx.x < H) rowstat[threadIdx.x] = stat;
         if (!__syncthreads_and(ok)) break;
-        const uint8_t* sx = sms + slot * ring.slot_bytes;
-        const uint8_t* sd = sms + slot2 * ring.slot_bytes;
-        const long long b = blockIdx.x + (long long)done * gridDim.x;
-        const int8_t* ex = CK ? p.exps + b * H * nblk : nullptr;
-        // z of the vector at column c of row r of the checkpoint
-        auto codes = [&](int r, int c, float2(&v)[NP]) {
-            uint32_t q[(V + 3) / 4];
-            ck8_load_shared<V>(sx + r * ldc + c, q);
-            ck8_values<V>(q, ck8_scale(__ldg(ex + r * nblk + c / kCk8Block)), v);
-        };
-        for (int h = warp; h < H; h += NW) {
-            const float mu = __ldg(p.mean + b * H + h), rs = __ldg(p.rstd + b * H + h);
+        mbar_try_wait(&bars[done & 1], phx);           // complete: each thread sees it for itself
+        mbar_try_wait(&bars[2], phd);
+        if (done + 1 < mine) load_x(done + 1);
+        const uint8_t* sx = sms + (done & 1) * ring.slot_bytes;
+        const uint8_t* sd = sms + 2 * ring.slot_bytes;
+        const int b = blockIdx.x + done * gridDim.x;
+        const int8_t* ex = CK ? p.exps + (size_t)b * H * nblk : nullptr;
+        for (int h = warp / PARTS; h < H; h += NW / PARTS) {
+            const float2 st = rowstat[h];
             float2 s1 = make_float2(0.f, 0.f), s2 = s1;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (lane + 32 * i) * V;
-                if (c < W) {
-                    float2 n[NP], d[NP], g[NP];
-                    Pack<T, V> w;
+            for (int i = 0; i < NVA; ++i) {
+                const int c = c0 + (lane + 32 * i) * VA;
+                if (c < c1) {
+                    float2 n[NPA], d[NPA], g[NPA];
+                    Pack<T, VA> w;
                     if constexpr (CK) {
-                        codes(h, c, n);
+                        uint32_t q[(VA + 3) / 4];
+                        ck8_load_shared<VA>(sx + h * ldc + c, q);
+                        ck8_values<VA>(q, ck8_scale(__ldg(ex + h * nblk + c / kCk8Block)), n);
                     } else {
-                        float2 r[NP];
+                        float2 r[NPA];
                         w.load_shared(sx + moff[i] + h * dh * ES);
                         w.get(n);
                         w.load_shared(sx + h * ld + c * ES);
                         w.get(r);
 #pragma unroll
-                        for (int k = 0; k < NP; ++k) n[k] = add2(n[k], r[k]);
+                        for (int k = 0; k < NPA; ++k) n[k] = add2(n[k], r[k]);
                     }
                     w.load_shared(sd + h * ld + c * ES);
                     w.get(d);
-                    staged<V>(sg, W, c, g);
+                    if constexpr (VA == V) {
+                        staged<V>(sg, W, c, g);
+                    } else {                           // half a vector of the staged layout
+                        const float4 a = *reinterpret_cast<const float4*>(sg + (c & 4 ? W / 2 : 0) + (c >> 3) * 4);
+                        g[0] = make_float2(a.x, a.y);
+                        g[NPA - 1] = make_float2(a.z, a.w);
+                    }
 #pragma unroll
-                    for (int k = 0; k < NP; ++k) {
-                        n[k] = mul2(add2(n[k], f2(-mu)), f2(rs));
+                    for (int k = 0; k < NPA; ++k) {
+                        n[k] = mul2(add2(n[k], f2(-st.x)), f2(st.y));
                         dg[i][k] = fma2(d[k], n[k], dg[i][k]);
                         db[i][k] = add2(db[i][k], d[k]);
                         const float2 dn = mul2(d[k], g[k]);
@@ -695,74 +756,114 @@ __global__ void __launch_bounds__(THREADS)
                 }
             }
             const float2 m = row_sum2<32>(make_float2(s1.x + s1.y, s2.x + s2.y), nullptr, turn);
-            if (lane == 0) rowc[h] = make_float4(rs, mu, -rs * (m.x * p.inv_w), -rs * rs * (m.y * p.inv_w));
+            if (lane == 0) rowsum[part * H + h] = m;
+        }
+        if (done + 1 < mine) fetch_stat(b + gridDim.x);
+        // the second step's pairs (t <= h): rows i and H-1-i of the triangle together are H + 1 pieces; the
+        // first two vectors of dy are on their way before the barriers, then always the next two
+        T* out = (T*)p.dx + (size_t)b * per;
+        const T* dyb = (const T*)p.dy + (size_t)b * per;
+        // piece k of folded row i, vector j of it: advanced by TH with carries
+        int j = j0, k = k0, i = i0, u = threadIdx.x;
+        struct Pair {
+            int t, h, j;                        // t < 0: none
+        };
+        Pair q[2];
+        Pack<T, V> wa[2], wb[2];
+        auto fetch = [&](int at) {
+            const bool low = k >= H - i;
+            Pair& c = q[at];
+            c.t = low ? H - 1 - i : i;
+            c.h = low ? k - 1 : i + k;          // t + k - (H - i), or i + k
+            c.j = j * V;
+            if (u >= npair || (low && c.t == i)) c.t = -1;     // odd H: the middle row is its own partner
+            if (c.t >= 0) {
+                wa[at].load(dyb + (c.t * W + c.h * dh + c.j));
+                wb[at].load(dyb + (c.h * W + c.t * dh + c.j));
+            }
+            u += TH;
+            j += dj;
+            k += dk;
+            i += di;
+            if (j >= vpd) { j -= vpd; ++k; }
+            if (k > H) { k -= H + 1; ++i; }
+        };
+        fetch(0);
+        fetch(1);
+        __syncthreads();
+        if (done + 1 < mine) load_d(done + 1);
+        if (threadIdx.x < H) {
+            float2 m = rowsum[threadIdx.x];
+            if (PARTS == 2) m = add2(m, rowsum[H + threadIdx.x]);
+            const float2 st = rowstat[threadIdx.x];
+            rowc[threadIdx.x] = make_float4(st.y, st.x, -st.y * (m.x * p.inv_w), -st.y * st.y * (m.y * p.inv_w));
         }
         __syncthreads();
-        // pairs (t <= h): rows i and H-1-i of the triangle together are H + 1 pieces
-        T* out = (T*)p.dx + b * per;
-        for (int u = threadIdx.x; u < npair; u += THREADS) {
-            const int k2 = vpd.div(u), j = (u - k2 * (int)vpd.d) * V;
-            const int i = hp1.div(k2), k = k2 - i * (H + 1);
-            int t, h;
-            if (k < H - i) {
-                t = i;
-                h = i + k;
-            } else {
-                t = H - 1 - i;
-                h = t + k - (H - i);
-                if (t == i) continue;                      // odd H: the middle row is its own partner
-            }
-            const int ca = h * dh + j, cb = t * dh + j;
+        // z of the vector at column c of row r of the checkpoint
+        auto codes = [&](int r, int c, float2(&v)[NP]) {
+            uint32_t q[(V + 3) / 4];
+            ck8_load_shared<V>(sx + r * ldc + c, q);
+            ck8_values<V>(q, ck8_scale(__ldg(ex + r * nblk + c / kCk8Block)), v);
+        };
+        auto step = [&](int at) {
+            const Pair c = q[at];
             float2 za[NP], zb[NP], da[NP], dd[NP], ga[NP], gb[NP];
-            Pack<T, V> w;
+            wa[at].get(da);
+            wb[at].get(dd);
+            fetch(at);
+            if (c.t < 0) return;
+            const int ca = c.h * dh + c.j, cb = c.t * dh + c.j;
             if constexpr (CK) {
-                codes(t, ca, za);
-                codes(h, cb, zb);
+                codes(c.t, ca, za);
+                codes(c.h, cb, zb);
             } else {
-                w.load_shared(sx + t * ld + ca * ES);
+                Pack<T, V> w;
+                w.load_shared(sx + c.t * ld + ca * ES);
                 w.get(za);
-                w.load_shared(sx + h * ld + cb * ES);
+                w.load_shared(sx + c.h * ld + cb * ES);
                 w.get(zb);
 #pragma unroll
-                for (int e = 0; e < NP; ++e) za[e] = zb[e] = add2(za[e], zb[e]);
+                for (int e = 0; e < NP; ++e) za[e] = add2(za[e], zb[e]);
             }
-            w.load_shared(sd + t * ld + ca * ES);
-            w.get(da);
-            w.load_shared(sd + h * ld + cb * ES);
-            w.get(dd);
             staged<V>(sg, W, ca, ga);
             staged<V>(sg, W, cb, gb);
-            const float4 ra = rowc[t], rb = rowc[h];
+            const float4 ra = rowc[c.t], rb = rowc[c.h];
             float2 o[NP];
+            if constexpr (CK) {
 #pragma unroll
-            for (int e = 0; e < NP; ++e) {
-                const float2 a = fma2(add2(za[e], f2(-ra.y)), f2(ra.w), fma2(mul2(da[e], ga[e]), f2(ra.x), f2(ra.z)));
-                const float2 c = fma2(add2(zb[e], f2(-rb.y)), f2(rb.w), fma2(mul2(dd[e], gb[e]), f2(rb.x), f2(rb.z)));
-                o[e] = add2(a, c);
+                for (int e = 0; e < NP; ++e) {
+                    const float2 a = fma2(add2(za[e], f2(-ra.y)), f2(ra.w), fma2(mul2(da[e], ga[e]), f2(ra.x), f2(ra.z)));
+                    const float2 d = fma2(add2(zb[e], f2(-rb.y)), f2(rb.w), fma2(mul2(dd[e], gb[e]), f2(rb.x), f2(rb.z)));
+                    o[e] = add2(a, d);
+                }
+            } else {
+                // one z: its two factors together, row h's centre expressed from row t's
+                const float2 wz = f2(ra.w + rb.w), cz = f2(ra.z + fmaf(ra.y - rb.y, rb.w, rb.z));
+#pragma unroll
+                for (int e = 0; e < NP; ++e)
+                    o[e] = fma2(mul2(da[e], ga[e]), f2(ra.x),
+                                fma2(mul2(dd[e], gb[e]), f2(rb.x), fma2(add2(za[e], f2(-ra.y)), wz, cz)));
             }
-            Pack<T, V>::store(out + (size_t)t * W + ca, o);
-            if (t != h) Pack<T, V>::store(out + (size_t)h * W + cb, o);
+            Pack<T, V>::store(out + (c.t * W + ca), o);
+            if (c.t != c.h) Pack<T, V>::store(out + (c.h * W + cb), o);
+        };
+        for (int v = threadIdx.x; v < npair; v += 2 * TH) {
+            step(0);
+            if (v + TH < npair) step(1);
         }
-        __syncthreads();
-        if (warp == 0) {
-            if (2 * done + nb < 2 * mine) load(2 * done + nb, slot);
-            if (2 * done + 1 + nb < 2 * mine) load(2 * done + 1 + nb, slot2);
-        }
-        slot += 2;
-        if (slot >= nb) { slot -= nb; ph ^= 1; }
     }
-    if (done < mine) {                       // given up: the loads in flight land before the block ends
-        if (threadIdx.x == 0)
-            for (int l = 2 * done; l < 2 * mine && l < 2 * done + nb; ++l) {
-                mbar_wait(&bars[slot], ph, 0x814);
-                if (++slot == nb) { slot = 0; ph ^= 1; }
-            }
+    if (done < mine) {
+        // given up, before anything of this sample was started: the loads in flight are its own two
+        if (threadIdx.x == 0) {
+            mbar_wait(&bars[done & 1], (done >> 1) & 1, 0x814);
+            mbar_wait(&bars[2], done & 1, 0x816);
+        }
         return;
     }
-    // the slots are free: every read is behind the last barrier
-    if (p.part) {
-        const int fit = (int)((size_t)nb * ring.slot_bytes / (W * sizeof(float)));
-        ln_store_partials<V, NV, 32>(p, reinterpret_cast<float*>(sms), min(fit, NW), NW, warp, lane, dg, db);
+    if (p.part) {                                // (its first barrier is behind every read of the slots)
+        const int fit = (int)((size_t)3 * ring.slot_bytes / (W * sizeof(float)));
+        ln_store_partials<VA, NVA, 32>(p, reinterpret_cast<float*>(sms), min(fit, NW / PARTS), NW / PARTS,
+                                       warp / PARTS, lane, c0, c1, dg, db);
     }
 }
 
@@ -936,21 +1037,24 @@ static uint32_t sample_ld(uint32_t bytes, uint32_t piece) {
     if (piece < 16) piece = 16;
     return bytes + (piece + 128 - bytes % 128) % 128;
 }
-// Slots of the ring, 4 at most (0: `need` do not fit): two blocks an SM where that leaves each a slot more
-// than it needs, so that loads run ahead.
-static int sample_slots(size_t slot, size_t extra, int need) {
-    const size_t half = (227 * 1024) / 2 - 1024 - extra, whole = kSampleSmem - extra;
-    int nb = (int)(half / slot);
-    if (nb < need + 1) nb = (int)(whole / slot);
-    return nb < need ? 0 : (nb > 4 ? 4 : nb);
+// Slots of the forward's ring, 4 at most (0: none fits): as many blocks an SM, up to 3, as leave each two
+// slots, so that loads run ahead.
+static int sample_slots(size_t slot, size_t extra) {
+    for (int blocks = 3; blocks >= 1; --blocks) {
+        const size_t room = blocks == 1 ? kSampleSmem : (227 * 1024) / blocks - 1024;
+        if (room <= extra) continue;
+        const int nb = (int)((room - extra) / slot);
+        if (nb >= 2 || (blocks == 1 && nb >= 1)) return nb > 4 ? 4 : nb;
+    }
+    return 0;
 }
 // Samples of at least 8 KB; smaller ones leave a block's threads idle, and the row kernels take them.
 constexpr size_t kSampleLeast = 8 * 1024;
 
 template <typename T, int V, int NV>
 static cudaError_t launch_sample_fwd(const NormParams& p, uint32_t ld, int nb, int sms, cudaStream_t st) {
-    constexpr int THREADS = 512;
-    auto kern = ln_sample_fwd_kernel<T, V, NV, THREADS>;
+    constexpr int NW = sample_warps(NV), THREADS = NW * 32 + 32;
+    auto kern = ln_sample_fwd_kernel<T, V, NV, NW>;
     static std::atomic<int> cache[64];
     int per_sm = 0;
     cudaError_t e = norm_resident(kern, THREADS, kSampleSmem, cache, &per_sm);
@@ -968,28 +1072,33 @@ static cudaError_t launch_sample_fwd_t(const NormParams& p, uint32_t ld, int nb,
     return cudaErrorInvalidValue;
 }
 
-template <typename T, int V, int NV, bool CK>
-static cudaError_t launch_sample_bwd(const NormParams& p, uint32_t ld, uint32_t ldc, int nb, int sms, int* nblk,
+static size_t sample_bwd_smem(int H, int W, uint32_t ld) {
+    return (size_t)3 * H * ld + W * sizeof(float) + H * (sizeof(float4) + 3 * sizeof(float2));
+}
+template <typename T, int VA, int NVA, int PARTS, bool CK, int NW>
+static cudaError_t launch_sample_bwd(const NormParams& p, uint32_t ld, uint32_t ldc, int sms, int* nblk,
                                      cudaStream_t st) {
-    constexpr int THREADS = 512;
-    auto kern = ln_sample_bwd_kernel<T, V, NV, CK, THREADS>;
+    constexpr int THREADS = NW * 32;
+    auto kern = ln_sample_bwd_kernel<T, VA, NVA, PARTS, CK, NW>;
     static std::atomic<int> cache[64];
     int per_sm = 0;
     cudaError_t e = norm_resident(kern, THREADS, kSampleSmem, cache, &per_sm);
     if (e != cudaSuccess) return e;
-    const size_t smem = (size_t)nb * p.map.banks * ld + p.map.W * sizeof(float) + p.map.banks * sizeof(float4);
+    const size_t smem = sample_bwd_smem(p.map.banks, p.map.W, ld);
     const long long grid = norm_blocks(p.B, 1, per_sm, smem, sms, kNormBlocksPerSm);
     *nblk = (int)grid;
-    kern<<<(unsigned)grid, THREADS, smem, st>>>(p, ld, ldc, nb, fast_div(p.map.dh / V), fast_div(p.map.banks + 1));
+    kern<<<(unsigned)grid, THREADS, smem, st>>>(p, ld, ldc);
     return cudaGetLastError();
 }
 template <typename T, bool CK>
-static cudaError_t launch_sample_bwd_t(const NormParams& p, uint32_t ld, uint32_t ldc, int nb, int sms, int* nblk,
+static cudaError_t launch_sample_bwd_t(const NormParams& p, uint32_t ld, uint32_t ldc, int sms, int* nblk,
                                        cudaStream_t st) {
-    constexpr int V = sizeof(T) == 2 ? 8 : 4;
-#define TM_ARGS (p, ld, ldc, nb, sms, nblk, st)
-    TM_NORM_WARP_ROWS(launch_sample_bwd, T, V, p.map.W, CK)
-#undef TM_ARGS
+    const int W = p.map.W;
+#define X(VA, NVA, PARTS, NW) \
+    if (W <= 32 * VA * NVA * PARTS) return launch_sample_bwd<T, VA, NVA, PARTS, CK, NW>(p, ld, ldc, sms, nblk, st);
+    if constexpr (sizeof(T) == 2) { X(8, 1, 1, 8) X(8, 2, 1, 8) X(8, 3, 1, 16) X(8, 4, 1, 16) }
+    else { X(4, 1, 1, 8) X(4, 2, 1, 8) X(4, 4, 1, 16) X(4, 8, 1, 16) }
+#undef X
     return cudaErrorInvalidValue;
 }
 
@@ -999,7 +1108,7 @@ cudaError_t launch_ln_fwd(int dtype, const NormParams& p, int sms, cudaStream_t 
     if (p.map.layout == 1 && p.res == p.x && p.map.T == p.map.banks && p.map.W <= 1024 &&
         (size_t)p.map.banks * p.map.W * esz >= kSampleLeast) {
         const uint32_t ld = sample_ld(p.map.W * esz, p.map.dh * esz);
-        const int nb = sample_slots((size_t)p.map.banks * ld, 2 * p.map.W * sizeof(float), 1);
+        const int nb = sample_slots((size_t)p.map.banks * ld, 2 * p.map.W * sizeof(float));
         if (nb) return dtype == 1 ? launch_sample_fwd_t<__nv_bfloat16>(p, ld, nb, sms, st)
                                   : launch_sample_fwd_t<float>(p, ld, nb, sms, st);
     }
@@ -1025,13 +1134,12 @@ cudaError_t launch_ln_bwd(int dtype, const NormParams& p, bool self, void* dgain
         const int esz = dtype == 1 ? 2 : 4;
         const bool vec = norm_vec(dtype, p.map.W);
         const uint32_t ld = sample_ld(p.map.W * esz, p.map.dh * esz), ldc = sample_ld(p.map.W, p.map.dh);
-        int nb = 0;
-        if (self && (size_t)p.map.banks * p.map.W * esz >= kSampleLeast && (!ck || p.map.W % 16 == 0))
-            nb = sample_slots((size_t)p.map.banks * ld, p.map.W * sizeof(float) + p.map.banks * sizeof(float4), 2);
+        const bool sample = self && (size_t)p.map.banks * p.map.W * esz >= kSampleLeast && (!ck || p.map.W % 16 == 0) &&
+                            sample_bwd_smem(p.map.banks, p.map.W, ld) <= kSampleSmem;
 #define X(FN, ...)                                                                                            \
     e = dtype == 1 ? (ck ? FN<__nv_bfloat16, true>(__VA_ARGS__) : FN<__nv_bfloat16, false>(__VA_ARGS__))      \
                    : (ck ? FN<float, true>(__VA_ARGS__) : FN<float, false>(__VA_ARGS__))
-        if (nb) X(launch_sample_bwd_t, p, ld, ldc, nb, sms, &nblk, st);
+        if (sample) X(launch_sample_bwd_t, p, ld, ldc, sms, &nblk, st);
         else if (self) X(launch_ln_self_t, p, sms, &nblk, st);
         else X(launch_ln_bwd_t, p, vec, sms, &nblk, st);
 #undef X
