@@ -148,7 +148,7 @@ cudaError_t launch_ln_fwd(int dtype, const NormParams& p, int sms, cudaStream_t 
 cudaError_t launch_ln_bwd(int dtype, const NormParams& p, bool self, void* dgain, void* dbias, int sms,
                           cudaStream_t st);
 cudaError_t launch_linear_simt(const SimtLin& p, cudaStream_t st);
-// Tensor maps of one contraction: operands, D (or fp32 partial sums), addend, z or codes (the last two
+// Tensor maps of one contraction: operands, D (or fp32 partial sums), addend, z (the last two
 // any valid map where they are not used)
 struct LinMaps {
     CUtensorMap a, b, o, r, z;

@@ -51,8 +51,8 @@ struct LinCfg {
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int EPI_WARPS = BN / 16;       // 4 lane quarters x BN / 64 column blocks
     static constexpr int NTHREADS = 32 * (2 + EPI_WARPS);
-    // an epilogue warp's boxes: 32 rows x 64 bf16 of D, beside it the same of z or the codes
-    static constexpr int BOX_BYTES = 4096 + (SAVE == LIN_KEEP_FULL ? 4096 : SAVE == LIN_KEEP_CK8 ? 2048 : 0);
+    // an epilogue warp's boxes: 32 rows x 64 bf16 of D, beside it the same of z
+    static constexpr int BOX_BYTES = SAVE == LIN_KEEP_FULL ? 8192 : 4096;
     static constexpr int STG_BYTES = EPI_WARPS * BOX_BYTES;
     static constexpr int BIAS_BYTES = 2 * BN * 4;   // the tile's bias in fp32, tiles in turn
     static constexpr int BAR_BYTES = 320;
@@ -138,7 +138,7 @@ __device__ __forceinline__ float2 lin_act2(float2 z) {
 }
 
 // D's rows are matrix rows, [bank][rows][cols], when A is MN-major (dW), else samples, [rows][bank][cols].
-// Maps: tmO D (or the fp32 partial sums), tmR the addend, tmZ z or the codes, all in boxes of 32 rows.
+// Maps: tmO D (or the fp32 partial sums), tmR the addend, tmZ z, all in boxes of 32 rows.
 template <int BN, bool PAIR, bool A_MN, bool B_MN, int ACT, int SAVE, bool F32OUT>
 __global__ void __launch_bounds__(LinCfg<BN, PAIR, SAVE>::NTHREADS, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -410,14 +410,20 @@ __global__ void __launch_bounds__(LinCfg<BN, PAIR, SAVE>::NTHREADS, 1)
                 } else {
                     if constexpr (SAVE == LIN_KEEP_CK8) {
                         // this lane's 32 columns are one block of its row (those past the row are zero: their
-                        // weights and bias were read as zero); 64 code bytes a row, 64-byte swizzle
+                        // weights and bias were read as zero); its codes go out from here, a whole sector
                         uint32_t qw[8];
                         e2[h] = ck8_quantize<32, 1>(reinterpret_cast<const float2(&)[16]>(v), qw);
-                        if (h == 0) free_box();
+                        if (row < p.rows) {
+                            int8_t* cp = p.codes + ((size_t)row * p.groups + ti.g) * p.cols + col0 + 32 * h;
+                            if ((p.cols & 15) == 0) {
+                                *reinterpret_cast<uint4*>(cp) = make_uint4(qw[0], qw[1], qw[2], qw[3]);
+                                if (32 * h + 16 < ncol) *reinterpret_cast<uint4*>(cp + 16) = make_uint4(qw[4], qw[5], qw[6], qw[7]);
+                            } else {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            *reinterpret_cast<uint4*>(box2 + lane * 64 + (((2 * h + i) ^ ((lane >> 1) & 3)) << 4)) =
-                                make_uint4(qw[4 * i], qw[4 * i + 1], qw[4 * i + 2], qw[4 * i + 3]);
+                                for (int i = 0; i < 4; ++i)
+                                    if (32 * h + 8 * i < ncol) *reinterpret_cast<uint2*>(cp + 8 * i) = make_uint2(qw[2 * i], qw[2 * i + 1]);
+                            }
+                        }
                     }
                     if constexpr (SAVE == LIN_KEEP_FULL) {
                         if (h == 0) free_box();
@@ -433,7 +439,7 @@ __global__ void __launch_bounds__(LinCfg<BN, PAIR, SAVE>::NTHREADS, 1)
                         v[2 * i] = o.x;
                         v[2 * i + 1] = o.y;
                     }
-                    if (SAVE == LIN_KEEP_NOTHING && !add && h == 0) free_box();
+                    if (SAVE != LIN_KEEP_FULL && !add && h == 0) free_box();
                     if (add) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -463,23 +469,9 @@ __global__ void __launch_bounds__(LinCfg<BN, PAIR, SAVE>::NTHREADS, 1)
                         if constexpr (OUT_MAT) tma_store_3d(&tmO, box, col0, row0, ti.g);
                         else tma_store_3d(&tmO, box, col0, ti.g, row0);
                         if constexpr (SAVE == LIN_KEEP_FULL) tma_store_3d(&tmZ, box2, col0, ti.g, row0);
-                        if constexpr (SAVE == LIN_KEEP_CK8)
-                            if ((p.cols & 15) == 0) tma_store_3d(&tmZ, box2, col0, ti.g, row0);
                         bulk_commit_group();
                     }
                     if constexpr (SAVE == LIN_KEEP_CK8) {
-                        if (p.cols & 15) {   // rows that are no multiple of 16 bytes have no tensor map: 8 at a time
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int r = 8 * i + (lane >> 2), c16 = lane & 3;
-                                const uint4 w = *reinterpret_cast<const uint4*>(box2 + r * 64 + ((c16 ^ ((r >> 1) & 3)) << 4));
-                                int8_t* cp = p.codes + ((size_t)(row0 + r) * p.groups + ti.g) * p.cols + col0 + 16 * c16;
-                                if (row0 + r < p.rows) {
-                                    if (16 * c16 < ncol) *reinterpret_cast<uint2*>(cp) = make_uint2(w.x, w.y);
-                                    if (16 * c16 + 8 < ncol) *reinterpret_cast<uint2*>(cp + 8) = make_uint2(w.z, w.w);
-                                }
-                            }
-                        }
                         if (row < p.rows) {
                             int8_t* ep = p.exps + ((size_t)row * p.groups + ti.g) * p.nblk + (col0 >> 5);
                             if ((p.nblk & 1) == 0) {

@@ -120,16 +120,6 @@ bool map_mats(CUtensorMap* m, const void* base, int banks, int R, int W, uint32_
               CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
     return map_3d(m, base, W, R, W, banks, (uint64_t)R * W, b0, b1, 1, swz);
 }
-bool map_codes(CUtensorMap* m, const void* base, int B, int banks, int W) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)W, (cuuint64_t)banks, (cuuint64_t)B};
-    cuuint64_t strides[2] = {(cuuint64_t)W, (cuuint64_t)banks * W};
-    cuuint32_t box[3] = {64, 1, 32}, es[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 bool map_mats_f32(CUtensorMap* m, const void* base, uint64_t mats, int R, int W) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
@@ -380,7 +370,6 @@ tm_status tm_pertoken_linear(const void* x, const void* residual, const tm_shape
     m.r = m.z = m.o;
     if (residual && !map_rows(&m.r, residual, g.B, g.banks, g.N, 64, 32)) return TM_ERR_CUDA;
     if (z_opt && !map_rows(&m.z, z_opt, g.B, g.banks, g.N, 64, 32)) return TM_ERR_CUDA;
-    if (save_opt && g.N % 16 == 0 && !map_codes(&m.z, save_opt->codes, g.B, g.banks, g.N)) return TM_ERR_CUDA;
     const int save = z_opt ? LIN_KEEP_FULL : save_opt ? LIN_KEEP_CK8 : LIN_KEEP_NOTHING;
     return cuda_status(launch_linear_fwd(pl.pair, w->act, save, m, p, num_sms(), st));
 }
