@@ -164,6 +164,28 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict_
     }
 }
 
+// The same for many parts of few columns (the bias gradient's): a block takes 32 columns, eight slices of the
+// parts side by side, then the slices in order.
+template <typename T>
+__global__ void __launch_bounds__(256) sum_parts_tall_kernel(const float* __restrict__ part, int R, long long n,
+                                                             T* __restrict__ out) {
+    __shared__ float sm[8][33];
+    const int cx = threadIdx.x & 31, sl = threadIdx.x >> 5;
+    const long long c = (long long)blockIdx.x * 32 + cx;
+    float s = 0.f;
+    if (c < n)
+#pragma unroll 8
+        for (int r = sl; r < R; r += 8) s += __ldg(part + r * n + c);
+    sm[sl][cx] = s;
+    __syncthreads();
+    if (sl == 0 && c < n) {
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += sm[i][cx];
+        from_f(s, out + c);
+    }
+}
+
 // ------------------------------------------------------------------ fp32 contractions
 // D[g][m][n] = sum_k A[g][m][k] B[g][n][k] with every stride given, 64 x 64 tiles, slabs of 16, 4 x 4
 // outputs a thread; the forward's epilogue as in tm_linear.cuh.
@@ -312,6 +334,12 @@ cudaError_t launch_linear_dw(bool pair, const LinMaps& m, const LinParams& p, in
 
 cudaError_t launch_sum_parts(int dtype, const float* part, int R, long long n, void* out, cudaStream_t st) {
     ProfileScope ps_("sum_parts", st);
+    if (R > 8 && n <= (1LL << 24)) {
+        const int grid = (int)((n + 31) / 32);
+        if (dtype == 1) sum_parts_tall_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(part, R, n, (__nv_bfloat16*)out);
+        else sum_parts_tall_kernel<float><<<grid, 256, 0, st>>>(part, R, n, (float*)out);
+        return cudaGetLastError();
+    }
     const long long per = (n & 3) == 0 ? n / 4 : n;
     const long long grid = (per + 255) / 256 < 148 * 16 ? (per + 255) / 256 : 148 * 16;
     if (dtype == 1) sum_parts_kernel<__nv_bfloat16><<<(int)grid, 256, 0, st>>>(part, R, n, (__nv_bfloat16*)out);
