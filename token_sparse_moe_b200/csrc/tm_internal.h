@@ -148,10 +148,10 @@ cudaError_t launch_ln_fwd(int dtype, const NormParams& p, int sms, cudaStream_t 
 cudaError_t launch_ln_bwd(int dtype, const NormParams& p, bool self, void* dgain, void* dbias, int sms,
                           cudaStream_t st);
 cudaError_t launch_linear_simt(const SimtLin& p, cudaStream_t st);
-// Tensor maps of one contraction: operands, D (or fp32 partial sums), addend, z (the last two
-// any valid map where they are not used)
+// Tensor maps of one contraction: operands, D (or fp32 partial sums), addend (any valid map where there is
+// none)
 struct LinMaps {
-    CUtensorMap a, b, o, r, z;
+    CUtensorMap a, b, o, r;
 };
 // pair: CTA pairs (tiles of 256 x 256), else 128 x 128
 cudaError_t launch_linear_fwd(bool pair, int act, int save, const LinMaps& m, const LinParams& p, int sms,

@@ -273,7 +273,7 @@ cudaError_t launch_linear_simt(const SimtLin& p, cudaStream_t st) {
 
 template <int BN, bool PAIR, bool A_MN, bool B_MN, int ACT, int SAVE, bool F32OUT>
 static cudaError_t launch_linear_one(const LinMaps& m, const LinParams& p, int sms, cudaStream_t st) {
-    using C = LinCfg<BN, PAIR, SAVE>;
+    using C = LinCfg<BN, PAIR>;
     auto kern = linear_gemm_kernel<BN, PAIR, A_MN, B_MN, ACT, SAVE, F32OUT>;
     static std::atomic<bool> configured[64];
     int dev = 0;
@@ -286,7 +286,7 @@ static cudaError_t launch_linear_one(const LinMaps& m, const LinParams& p, int s
     }
     ProfileScope ps_(A_MN ? "linear_dw" : B_MN ? "linear_dx" : "linear", st);
     if (!PAIR) {
-        kern<<<p.ntile < sms ? p.ntile : sms, C::NTHREADS, C::SMEM_BYTES, st>>>(m.a, m.b, m.o, m.r, m.z, p);
+        kern<<<p.ntile < sms ? p.ntile : sms, C::NTHREADS, C::SMEM_BYTES, st>>>(m.a, m.b, m.o, m.r, p);
         return cudaGetLastError();
     }
     cudaLaunchConfig_t cfg;
@@ -302,7 +302,7 @@ static cudaError_t launch_linear_one(const LinMaps& m, const LinParams& p, int s
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, m.a, m.b, m.o, m.r, m.z, p);
+    return cudaLaunchKernelEx(&cfg, kern, m.a, m.b, m.o, m.r, p);
 }
 
 // The two shapes of tile: pairs of 256 x 256, single CTAs of 128 x 128.

@@ -37,13 +37,15 @@ struct LinParams {
     int ntile;                 // groups * splits * mt * nt
     int split_slabs;           // slabs of 64 of a run, at most
     const __nv_bfloat16* bias;   // [groups, cols] or NULL
-    int add;                   // residual / dx_add in D's layout (its map: tmR)
+    int add;                   // residual / dx_add in D's layout (its map: tmR), and
+    const __nv_bfloat16* res;  // its address
+    __nv_bfloat16* z;          // LIN_KEEP_FULL: [rows * groups, cols]
     int8_t* codes;             // LIN_KEEP_CK8: [rows * groups, cols], and
     int8_t* exps;              //               [rows * groups, nblk]
     int nblk;
 };
 
-template <int BN, bool PAIR, int SAVE>
+template <int BN, bool PAIR>
 struct LinCfg {
     static constexpr int BM = 128;                  // rows of D per CTA (a pair: 256)
     static constexpr int BC = PAIR ? BN / 2 : BN;   // B rows that this CTA loads
@@ -51,8 +53,8 @@ struct LinCfg {
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int EPI_WARPS = BN / 16;       // 4 lane quarters x BN / 64 column blocks
     static constexpr int NTHREADS = 32 * (2 + EPI_WARPS);
-    // an epilogue warp's boxes: 32 rows x 64 bf16 of D, beside it the same of z
-    static constexpr int BOX_BYTES = SAVE == LIN_KEEP_FULL ? 8192 : 4096;
+    // an epilogue warp's box: 32 rows x 64 bf16 of D
+    static constexpr int BOX_BYTES = 4096;
     static constexpr int STG_BYTES = EPI_WARPS * BOX_BYTES;
     static constexpr int BIAS_BYTES = 2 * BN * 4;   // the tile's bias in fp32, tiles in turn
     static constexpr int BAR_BYTES = 320;
@@ -138,13 +140,13 @@ __device__ __forceinline__ float2 lin_act2(float2 z) {
 }
 
 // D's rows are matrix rows, [bank][rows][cols], when A is MN-major (dW), else samples, [rows][bank][cols].
-// Maps: tmO D (or the fp32 partial sums), tmR the addend, tmZ z, all in boxes of 32 rows.
+// Maps: tmO D (or the fp32 partial sums), tmR the addend, in boxes of 32 rows.
 template <int BN, bool PAIR, bool A_MN, bool B_MN, int ACT, int SAVE, bool F32OUT>
-__global__ void __launch_bounds__(LinCfg<BN, PAIR, SAVE>::NTHREADS, 1)
+__global__ void __launch_bounds__(LinCfg<BN, PAIR>::NTHREADS, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmR,
-                       const __grid_constant__ CUtensorMap tmZ, const LinParams p) {
-    using C = LinCfg<BN, PAIR, SAVE>;
+                       const LinParams p) {
+    using C = LinCfg<BN, PAIR>;
     constexpr int STAGES = C::STAGES;
     constexpr bool OUT_MAT = A_MN;
     const int rank = PAIR ? (int)cluster_ctarank() : 0;
@@ -324,7 +326,6 @@ __global__ void __launch_bounds__(LinCfg<BN, PAIR, SAVE>::NTHREADS, 1)
         // receives the addend by TMA, then each lane turns its row into D's, then a bulk store takes it.
         const int q = warp & 3, cb = ((warp - 2) >> 2) * 64;
         uint8_t* box = smem + C::OFF_STG + (warp - 2) * C::BOX_BYTES;
-        uint8_t* box2 = box + 4096;
         uint64_t* addb = &add_full[warp - 2];
         auto at = [&](uint8_t* b, int c16) -> uint8_t* { return b + lane * 128 + ((c16 ^ (lane & 7)) << 4); };
         int lt = 0;
@@ -337,7 +338,8 @@ __global__ void __launch_bounds__(LinCfg<BN, PAIR, SAVE>::NTHREADS, 1)
             const int col0 = ti.n * BN + cb;
             // columns of this warp inside D (none where its rows are past the extent): uniform in the warp
             const int ncol = row0 < p.rows ? min(64, p.cols - col0) : 0;
-            const bool add = !F32OUT && p.add && ncol > 0;
+            // (where z is kept whole the box is its first, and a lane reads its row of the addend from memory)
+            const bool add = !F32OUT && SAVE != LIN_KEEP_FULL && p.add && ncol > 0;
             // the box is free once the last tile's store has read it; without an addend that is waited for
             // as late as the first write
             auto free_box = [&]() {
@@ -368,6 +370,7 @@ __global__ void __launch_bounds__(LinCfg<BN, PAIR, SAVE>::NTHREADS, 1)
             __syncwarp();
             const uint32_t taddr = tmem_base + (uint32_t(q * 32) << 16) + buf * BN + cb;
             int e2[2] = {0, 0};              // exponents of the row's two blocks
+            uint32_t y[SAVE == LIN_KEEP_FULL ? 32 : 1];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float v[32];
@@ -411,6 +414,7 @@ __global__ void __launch_bounds__(LinCfg<BN, PAIR, SAVE>::NTHREADS, 1)
                     if constexpr (SAVE == LIN_KEEP_CK8) {
                         // this lane's 32 columns are one block of its row (those past the row are zero: their
                         // weights and bias were read as zero); its codes go out from here, a whole sector
+                        // (through the box, in 64-byte row pieces, the copying cost as much as it saved)
                         uint32_t qw[8];
                         e2[h] = ck8_quantize<32, 1>(reinterpret_cast<const float2(&)[16]>(v), qw);
                         if (row < p.rows) {
@@ -418,7 +422,7 @@ __global__ void __launch_bounds__(LinCfg<BN, PAIR, SAVE>::NTHREADS, 1)
                             if ((p.cols & 15) == 0) {
                                 *reinterpret_cast<uint4*>(cp) = make_uint4(qw[0], qw[1], qw[2], qw[3]);
                                 if (32 * h + 16 < ncol) *reinterpret_cast<uint4*>(cp + 16) = make_uint4(qw[4], qw[5], qw[6], qw[7]);
-                            } else {
+                            } else {                                          // rows that start 8 bytes off
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
                                     if (32 * h + 8 * i < ncol) *reinterpret_cast<uint2*>(cp + 8 * i) = make_uint2(qw[2 * i], qw[2 * i + 1]);
@@ -426,10 +430,11 @@ __global__ void __launch_bounds__(LinCfg<BN, PAIR, SAVE>::NTHREADS, 1)
                         }
                     }
                     if constexpr (SAVE == LIN_KEEP_FULL) {
+                        // z goes into the box first, y stays in registers until z is copied out
                         if (h == 0) free_box();
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            *reinterpret_cast<uint4*>(at(box2, 4 * h + i)) =
+                            *reinterpret_cast<uint4*>(at(box, 4 * h + i)) =
                                 make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
                                            pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
                     }
@@ -454,11 +459,51 @@ __global__ void __launch_bounds__(LinCfg<BN, PAIR, SAVE>::NTHREADS, 1)
                             }
                         }
                     }
+                    if constexpr (SAVE == LIN_KEEP_FULL) {
+                        if (p.add && row < p.rows) {
+                            const __nv_bfloat16* rp = p.res + ((size_t)row * p.groups + ti.g) * p.cols + col0 + 32 * h;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4*>(at(box, 4 * h + i)) =
-                            make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                                       pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+                            for (int i = 0; i < 4; ++i) {
+                                if (32 * h + 8 * i < ncol) {
+                                    const uint4 w = __ldg(reinterpret_cast<const uint4*>(rp + 8 * i));
+                                    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        v[8 * i + 2 * k] += bf16_lo(a[k]);
+                                        v[8 * i + 2 * k + 1] += bf16_hi(a[k]);
+                                    }
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) y[16 * h + i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<uint4*>(at(box, 4 * h + i)) =
+                                make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                                           pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+                    }
+                }
+            }
+            if constexpr (SAVE == LIN_KEEP_FULL) {
+                if (ncol > 0) {
+                    // z leaves the box in whole 128-byte row pieces, four rows a store, then y takes its place
+                    // (a second box for z took the operand ring from five stages to three: 30 % of the large layer)
+                    __syncwarp();
+                    const int rl = lane >> 3, c16 = lane & 7;
+                    const size_t rs = (size_t)p.groups * p.cols;
+                    __nv_bfloat16* zp = p.z + ((size_t)(row0 + rl) * p.groups + ti.g) * p.cols + col0 + c16 * 8;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 4 * i + rl;
+                        const uint4 w = *reinterpret_cast<const uint4*>(box + r * 128 + ((c16 ^ (r & 7)) << 4));
+                        if (c16 * 8 < ncol && row0 + r < p.rows) *reinterpret_cast<uint4*>(zp + 4 * i * rs) = w;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4*>(at(box, i)) = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
                 }
             }
             if constexpr (!F32OUT) {
@@ -468,7 +513,6 @@ __global__ void __launch_bounds__(LinCfg<BN, PAIR, SAVE>::NTHREADS, 1)
                     if (lane == 0) {
                         if constexpr (OUT_MAT) tma_store_3d(&tmO, box, col0, row0, ti.g);
                         else tma_store_3d(&tmO, box, col0, ti.g, row0);
-                        if constexpr (SAVE == LIN_KEEP_FULL) tma_store_3d(&tmZ, box2, col0, ti.g, row0);
                         bulk_commit_group();
                     }
                     if constexpr (SAVE == LIN_KEEP_CK8) {

@@ -360,6 +360,8 @@ tm_status tm_pertoken_linear(const void* x, const void* residual, const tm_shape
     LinParams p = lin_params(g.banks, g.B, g.N, g.K, pl);
     p.bias = (const __nv_bfloat16*)w->bias;
     p.add = residual != nullptr;
+    p.res = (const __nv_bfloat16*)residual;
+    p.z = (__nv_bfloat16*)z_opt;
     p.codes = save_opt ? save_opt->codes : nullptr;
     p.exps = save_opt ? save_opt->exps : nullptr;
     p.nblk = (g.N + kCk8Block - 1) / kCk8Block;
@@ -367,9 +369,8 @@ tm_status tm_pertoken_linear(const void* x, const void* residual, const tm_shape
     if (!map_rows(&m.a, x, g.B, g.banks, g.K, 64, 128) || !map_mats(&m.b, w->w, g.banks, g.N, g.K, 64, 128) ||
         !map_rows(&m.o, y, g.B, g.banks, g.N, 64, 32))
         return TM_ERR_CUDA;
-    m.r = m.z = m.o;
+    m.r = m.o;
     if (residual && !map_rows(&m.r, residual, g.B, g.banks, g.N, 64, 32)) return TM_ERR_CUDA;
-    if (z_opt && !map_rows(&m.z, z_opt, g.B, g.banks, g.N, 64, 32)) return TM_ERR_CUDA;
     const int save = z_opt ? LIN_KEEP_FULL : save_opt ? LIN_KEEP_CK8 : LIN_KEEP_NOTHING;
     return cuda_status(launch_linear_fwd(pl.pair, w->act, save, m, p, num_sms(), st));
 }
@@ -451,7 +452,7 @@ tm_status tm_pertoken_linear_backward(const void* x, const void* dy, const void*
         if (!map_rows(&m.a, dz, g.B, g.banks, g.N, 64, 128) || !map_mats(&m.b, w->w, g.banks, g.N, g.K, 64, 64) ||
             !map_rows(&m.o, dx, g.B, g.banks, g.K, 64, 32))
             return TM_ERR_CUDA;
-        m.r = m.z = m.o;
+        m.r = m.o;
         if (dx_add && !map_rows(&m.r, dx_add, g.B, g.banks, g.K, 64, 32)) return TM_ERR_CUDA;
         if ((s = cuda_status(launch_linear_dx(pl.pair, m, p, num_sms(), st))) != TM_OK) return s;
     }
@@ -463,7 +464,7 @@ tm_status tm_pertoken_linear_backward(const void* x, const void* dy, const void*
         if (pl.splits > 1 ? !map_mats_f32(&m.o, ws.dw, (uint64_t)pl.splits * g.banks, g.N, g.K)
                           : !map_mats(&m.o, dw, g.banks, g.N, g.K, 64, 32))
             return TM_ERR_CUDA;
-        m.r = m.z = m.o;
+        m.r = m.o;
         if ((s = cuda_status(launch_linear_dw(pl.pair, m, p, num_sms(), st))) != TM_OK) return s;
         if (pl.splits > 1)
             return cuda_status(launch_sum_parts(g.dtype, ws.dw, pl.splits, cols * g.K, dw, st));
