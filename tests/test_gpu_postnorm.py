@@ -97,7 +97,8 @@ def test_layer_norm_rows(dtype, B, banks, W, with_res, ckpt):
     check("dbias", grads["dbias"], b["dbias"], tb)
 
 
-MIXED = [(1, 2, 16, 2), (5, 8, 64, 8), (3, 4, 96, 2), (2, 3, 64, 8), (7, 16, 256, 16), (3, 32, 512, 32), (2, 48, 768, 48),
+# (33 tokens of 264: checkpoint rows that are no multiple of 16 bytes; one token, one head)
+MIXED = [(1, 2, 16, 2), (4, 1, 16, 1), (2, 33, 264, 33), (9, 20, 480, 20), (2, 24, 768, 24), (5, 8, 64, 8), (3, 4, 96, 2), (2, 3, 64, 8), (7, 16, 256, 16), (3, 32, 512, 32), (2, 48, 768, 48),
          (300, 5, 80, 5)]
 
 
@@ -196,6 +197,254 @@ def test_linear_bf16(B, banks, K, N, act, bias_, res_, save):
 @pytest.mark.parametrize("B,banks,K,N", LINEAR_F32)
 def test_linear_f32(B, banks, K, N, act, bias_, res_, save):
     linear_case("f32", B, banks, K, N, act, bias_, res_, save)
+
+
+# ------------------------------------------------------------------ calls that the cases above do not make
+def guarded(shape_, dtype, device=DEV):
+    """A tensor between two stretches of a byte pattern: (tensor, check that they are intact)."""
+    n = int(np.prod(shape_)) * torch.empty(0, dtype=dtype).element_size()
+    pad = 4096
+    buf = torch.full((n + 2 * pad,), 0x5A, dtype=torch.uint8, device=device)
+    t = buf[pad:pad + n].view(dtype).view(shape_)
+    return t, lambda: bool((buf[:pad] == 0x5A).all()) and bool((buf[pad + n:] == 0x5A).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_nothing_is_written_beside_the_outputs(dtype):
+    rng = np.random.default_rng(3)
+    B, banks, K, N, T = 131, 3, 72, 200, 24
+    x, _ = draw(rng, (B, banks, K), dtype)
+    w, _ = draw(rng, (banks, N, K), dtype)
+    dy, _ = draw(rng, (B, banks, N), dtype)
+    lin = api.Linear(w, None, "gelu")
+    checks = []
+
+    def out(shape_, dt=DT[dtype]):
+        t, ok = guarded(shape_, dt)
+        checks.append(ok)
+        return t
+    y, z, codes, exps = out((B, banks, N)), out((B, banks, N)), out((B, banks, N), torch.int8), out((B, banks, 7), torch.int8)
+    sh, c = api.shape(B, banks, K, 1, DT[dtype]), lin.c(banks, K, DT[dtype], 0)
+    for kept in ({"z": z}, {"save": A.tm_ckpt8(codes.data_ptr(), exps.data_ptr())}):
+        assert api.lib().tm_pertoken_linear(x.data_ptr(), None, sh, c, y.data_ptr(), kept.get("z", z).data_ptr() if "z" in kept else None,
+                                            kept.get("save"), None) == 0
+    dx, dw = out((B, banks, K)), out((banks, N, K))
+    n = api.lib().tm_pertoken_linear_backward_workspace_bytes(sh, c)
+    ws = out((n,), torch.uint8)
+    assert api.lib().tm_pertoken_linear_backward(x.data_ptr(), dy.data_ptr(), z.data_ptr(), None, None, sh, c, dx.data_ptr(),
+                                                 A.tm_linear_grads(dw.data_ptr(), None), ws.data_ptr(), n, None) == 0
+    # norms: rows, and samples of both sizes
+    for layout, Bn, bk, W in ((A.TM_LAYOUT_ROWS, 131, 3, 72), (A.TM_LAYOUT_MIXED, 7, T, T * 8), (A.TM_LAYOUT_MIXED, 7, 6, 96)):
+        xs, _ = draw(rng, (Bn, bk, W), dtype)
+        ds, _ = draw(rng, (Bn, bk, W), dtype)
+        mixed = layout == A.TM_LAYOUT_MIXED
+        shn = api.shape(Bn, bk, W, bk if mixed else 1, DT[dtype], EPS)
+        wn = A.tm_layer_norm_w(bk, W, None, None)
+        yn, mean, rstd = out((Bn, bk, W)), out((Bn * bk,), torch.float32), out((Bn * bk,), torch.float32)
+        ck = A.tm_ckpt8(out((Bn, bk, W), torch.int8).data_ptr(), out((Bn, bk, (W + 31) // 32), torch.int8).data_ptr())
+        assert api.lib().tm_layer_norm(xs.data_ptr(), xs.data_ptr(), layout, shn, wn, yn.data_ptr(), mean.data_ptr(),
+                                       rstd.data_ptr(), ck, None) == 0
+        n = api.lib().tm_layer_norm_backward_workspace_bytes(shn, layout, wn)
+        dxn, dg, db, ws = out((Bn, bk, W)), out((W,)), out((W,)), out((n,), torch.uint8)
+        for saved in (None, ck):
+            assert api.lib().tm_layer_norm_backward(xs.data_ptr(), xs.data_ptr(), saved, mean.data_ptr(), rstd.data_ptr(),
+                                                    ds.data_ptr(), layout, shn, wn, 1 if mixed else 0, dxn.data_ptr(), None,
+                                                    A.tm_layer_norm_grads(dg.data_ptr(), db.data_ptr()), ws.data_ptr(), n,
+                                                    None) == 0
+        for width in (W, 45):
+            xp = xs.reshape(-1)[:Bn * bk * 45].reshape(-1, 45) if width == 45 else xs
+            cp = A.tm_ckpt8(out(xp.shape, torch.int8).data_ptr(), out((xp.numel() // width, (width + 31) // 32), torch.int8).data_ptr())
+            back = out(xp.shape)
+            assert api.lib().tm_checkpoint8_pack(xp.data_ptr(), A.TM_BF16 if dtype == "bf16" else A.TM_F32, xp.numel() // width,
+                                                 width, cp, None) == 0
+            assert api.lib().tm_checkpoint8_unpack(cp, A.TM_BF16 if dtype == "bf16" else A.TM_F32, xp.numel() // width, width,
+                                                   back.data_ptr(), None) == 0
+    torch.cuda.synchronize()
+    assert all(ok() for ok in checks)
+
+
+def chain(x, lin1, lin2, g, dy, sh, kept):
+    """Every operator once, as a post-norm block's training step runs them."""
+    s, n1 = api.layer_norm(x, x, A.TM_LAYOUT_MIXED, sh, g[0], g[1], checkpoint8=kept == "ckpt8")
+    h, z = api.pertoken_linear(s, lin1, save=kept)
+    o = api.pertoken_linear(h, lin2, residual=s)
+    y, n2 = api.layer_norm(o, None, A.TM_LAYOUT_ROWS, sh, g[2], g[3], checkpoint8=kept == "ckpt8")
+    do, _, g2 = api.layer_norm_backward(dy, n2, A.TM_LAYOUT_ROWS, sh, g[2], x=o)
+    dh, w2 = api.pertoken_linear_backward(h, do, lin2)
+    ds, w1 = api.pertoken_linear_backward(s, dh, lin1, z, dx_add=do)
+    dx, _, g1 = api.layer_norm_backward(ds, n1, A.TM_LAYOUT_MIXED, sh, g[0], x=x, residual=x, residual_is_x=True)
+    return {"s": s, "h": h, "o": o, "y": y, "do": do, "dh": dh, "ds": ds, "dx": dx, "dw1": w1["dw"], "db1": w1["db"],
+            "dw2": w2["dw"], "db2": w2["db"], "dg1": g1["dgain"], "dg2": g2["dgain"]}
+
+
+def chain_inputs(B, T, D, F, seed=1):
+    rng = np.random.default_rng(seed)
+    x, xo = draw(rng, (B, T, D), "bf16")
+    w1, w1o = draw(rng, (T, F, D), "bf16", std=D ** -0.5)
+    w2, w2o = draw(rng, (T, D, F), "bf16", std=F ** -0.5)
+    b1, b1o = draw(rng, (T, F), "bf16", std=0.1)
+    b2, b2o = draw(rng, (T, D), "bf16", std=0.1)
+    g = [draw(rng, (D,), "bf16", std=0.1, mean=m) for m in (1.0, 0.0, 1.0, 0.0)]
+    dy, dyo = draw(rng, (B, T, D), "bf16")
+    dev = (x, api.Linear(w1, b1, "gelu"), api.Linear(w2, b2), [v[0] for v in g], dy, api.shape(B, T, D, T, "bf16", EPS))
+    return dev, (xo, w1o, b1o, w2o, b2o, [v[1] for v in g], dyo)
+
+
+def bf16(a):
+    return torch.from_numpy(a).to(torch.bfloat16).double().numpy()
+
+
+def oracle_chain(xo, w1, b1, w2, b2, g, dy, kept, store):
+    """The block in float64; `store` rounds what the library stores, and the kept tensors go through 8 bits."""
+    T = xo.shape[1]
+    z1 = P.mix_rows(xo, T) + xo
+    f1 = P.layer_norm(z1, g[0], g[1], EPS)
+    s = store(f1["y"])
+    h, zp = P.linear(s, w1, b1, "gelu")
+    h = store(h)
+    o = store(P.linear(h, w2, b2, "none", s)[0])
+    f2 = P.layer_norm(o, g[2], g[3], EPS)
+    q = (lambda v: P.checkpoint8(v)[2]) if kept == "ckpt8" and store is bf16 else (lambda v: store(v))
+    n2 = P.layer_norm_backward(q(o), dy, g[2], f2["mean"], f2["rstd"])
+    do = store(n2["dz"])
+    l2 = P.linear_backward(h, do, o, w2, "none")
+    dh = store(l2["dx"])
+    zk = q(zp)
+    l1 = P.linear_backward(s, dh, zk, w1, "gelu")
+    dz = store(l1["dz"])
+    ds = store(np.einsum("bgn,gnk->bgk", dz, w1) + do)
+    dw1 = np.einsum("bgn,bgk->gnk", dz, s)
+    n1 = P.layer_norm_backward(q(z1) if kept == "ckpt8" else z1, ds, g[0], f1["mean"], f1["rstd"])
+    dx = n1["dz"] + P.revert_rows(n1["dz"], T)
+    return {"s": s, "h": h, "o": o, "y": f2["y"], "do": do, "dh": dh, "ds": ds, "dx": dx, "dw1": dw1, "db1": l1["db"],
+            "dw2": l2["dw"], "db2": l2["db"], "dg1": n1["dgain"], "dg2": n2["dgain"]}
+
+
+@pytest.mark.parametrize("kept", ["full", "ckpt8"])
+def test_post_norm_block_training_step(kept):
+    """S = LN(Mix(X) + X); Y = LN(gelu(S W1^T + b1) W2^T + b2 + S) and its whole backward pass, operator by
+    operator.  Against the exact block in float64 the library's outputs may be as far off (in rms) as a
+    float64 model that rounds what the library stores (and quantises what it keeps in 8 bits), plus half of
+    that again: roundings of the same size at the same places fall differently, their rms does not."""
+    dev, host = chain_inputs(70, 16, 256, 384)
+    got = chain(*dev, kept)
+    exact = oracle_chain(*host, kept, lambda v: v)
+    model = oracle_chain(*host, kept, bf16)
+    for k, o in exact.items():
+        rms = np.sqrt(np.mean(o * o))
+        off = np.sqrt(np.mean((f64(got[k]) - o) ** 2)) / rms
+        by_model = np.sqrt(np.mean((bf16(model[k]) - o) ** 2)) / rms
+        assert off <= 1.5 * by_model, (k, off, by_model)
+
+
+def test_same_bits_twice_in_a_graph_and_on_two_streams():
+    dev, _ = chain_inputs(150, 16, 256, 264)
+    x = dev[0]
+    first = {k: v.clone() for k, v in chain(*dev, "ckpt8").items()}
+    again = chain(*dev, "ckpt8")
+    assert all(torch.equal(first[k], again[k]) for k in first)
+    # captured: the replay works on what the inputs hold then
+    keep = x.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain(*dev, "ckpt8")
+    x.copy_(keep.flip(0))
+    graph.replay()
+    torch.cuda.synchronize()
+    flipped = {k: v.clone() for k, v in out.items()}
+    ref = chain(*dev, "ckpt8")
+    assert all(torch.equal(flipped[k], ref[k]) for k in ref)
+    x.copy_(keep)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(out[k], first[k]) for k in first)
+    # two streams at once, each with workspaces of its own
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            outs.append([chain(*dev, "ckpt8") for _ in range(3)][-1])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o[k], first[k]) for o in outs for k in first)
+    # the stream argument, while another stream is the current one
+    y, saved = api.layer_norm(x, x, A.TM_LAYOUT_MIXED, dev[5], *dev[3][:2], checkpoint8=True, stream=streams[0])
+    h, z = api.pertoken_linear(y, dev[1], save="full", stream=streams[0])
+    streams[0].synchronize()
+    assert torch.equal(y, first["s"]) and torch.equal(h, first["h"])
+
+
+def test_a_bad_value_stays_in_its_sample():
+    """NaN and infinity in one sample reach that sample's outputs and the sums over samples, nothing else; a
+    checkpoint does not hide them from the backward pass."""
+    rng = np.random.default_rng(8)
+    B, banks, K, N = 140, 2, 64, 136
+    x, _ = draw(rng, (B, banks, K), "bf16")
+    w, _ = draw(rng, (banks, N, K), "bf16")
+    dy, _ = draw(rng, (B, banks, N), "bf16")
+    sh = api.shape(B, banks, K, 1, "bf16", EPS)
+    clean = api.pertoken_linear(x, api.Linear(w, None, "silu"))
+    for bad in (float("nan"), float("inf")):
+        xb = x.clone()
+        xb[77, 1, 5] = bad
+        lin = api.Linear(w, None, "silu")
+        y, ck = api.pertoken_linear(xb, lin, save="ckpt8")
+        rows = ~torch.isfinite(y).all(-1)
+        assert rows.nonzero().tolist() == [[77, 1]] and torch.equal(y[~rows], clean[~rows])
+        back = api.checkpoint8_unpack(ck)
+        assert (~torch.isfinite(back).all(-1)).nonzero().tolist() == [[77, 1]]
+        dx, g = api.pertoken_linear_backward(xb, dy, lin, ck)
+        assert (~torch.isfinite(dx).all(-1)).nonzero().tolist() == [[77, 1]]
+        assert torch.isfinite(g["dw"][0]).all() and not torch.isfinite(g["dw"][1]).any()
+        yn, saved = api.layer_norm(xb, None, A.TM_LAYOUT_ROWS, sh, checkpoint8=True)
+        assert (~torch.isfinite(yn).all(-1)).nonzero().tolist() == [[77, 1]]
+        dn, _, _ = api.layer_norm_backward(yn.nan_to_num(), saved, A.TM_LAYOUT_ROWS, sh)
+        assert (~torch.isfinite(dn).all(-1)).nonzero().tolist() == [[77, 1]]
+
+
+def test_gain_and_bias_may_be_absent_and_gradients_not_wanted():
+    rng = np.random.default_rng(9)
+    x, xo = draw(rng, (9, 2, 96), "bf16")
+    dy, do = draw(rng, (9, 2, 96), "bf16")
+    sh, w = api.shape(9, 2, 96, 1, "bf16", EPS), A.tm_layer_norm_w(2, 96, None, None)
+    f = P.layer_norm(xo, None, None, EPS)
+    y, saved = api.layer_norm(x, None, A.TM_LAYOUT_ROWS, sh)
+    check("y", y, f["y"], norm_tols(xo, f, None, None, "bf16")[3])
+    dx, _, grads = api.layer_norm_backward(dy, saved, A.TM_LAYOUT_ROWS, sh, x=x)
+    dx2, y2 = torch.empty_like(x), torch.empty_like(x)
+    assert api.lib().tm_layer_norm_backward(x.data_ptr(), None, None, saved.mean.data_ptr(), saved.rstd.data_ptr(), dy.data_ptr(),
+                                            A.TM_LAYOUT_ROWS, sh, w, 0, dx2.data_ptr(), None, None, None, 0, None) == 0
+    assert api.lib().tm_layer_norm(x.data_ptr(), None, A.TM_LAYOUT_ROWS, sh, w, y2.data_ptr(), None, None, None, None) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(dx, dx2) and torch.equal(y, y2)
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: the last rows come out as they do alone."""
+    B, banks, W, N = 290000, 48, 160, 8
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.empty(B, banks, W, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    assert x.numel() > 2 ** 31
+    sh, tail_sh = api.shape(B, banks, W, 1, "bf16", EPS), api.shape(3, banks, W, 1, "bf16", EPS)
+    tail = x[-3:].clone()
+    ck = api.checkpoint8_pack(x)
+    assert torch.equal(ck.codes[-3:], api.checkpoint8_pack(tail).codes)
+    assert torch.equal(api.checkpoint8_unpack(ck)[-3:], api.checkpoint8_unpack(api.checkpoint8_pack(tail)))
+    del ck
+    y, saved = api.layer_norm(x, None, A.TM_LAYOUT_ROWS, sh)
+    yt, st = api.layer_norm(tail, None, A.TM_LAYOUT_ROWS, tail_sh)
+    assert torch.equal(y[-3:], yt) and torch.equal(saved.mean[-3:], st.mean)
+    dx, _, _ = api.layer_norm_backward(x, saved, A.TM_LAYOUT_ROWS, sh, x=x, dx=y)
+    dt, _, _ = api.layer_norm_backward(tail, st, A.TM_LAYOUT_ROWS, tail_sh, x=tail)
+    assert torch.equal(dx[-3:], dt)
+    del y, dx
+    lin = api.Linear(torch.empty(banks, N, W, dtype=torch.bfloat16, device=DEV).normal_(generator=g).mul_(0.1), None, "relu")
+    out, z = api.pertoken_linear(x, lin, save="full")
+    ot = api.pertoken_linear(tail, lin)
+    assert torch.equal(out[-3:], ot)
+    dxl, _ = api.pertoken_linear_backward(x, out, lin, z)
+    dlt, _ = api.pertoken_linear_backward(tail, ot, lin, z[-3:])
+    assert torch.equal(dxl[-3:], dlt)
 
 
 def test_no_device_error_was_recorded():

@@ -1017,6 +1017,8 @@ def layer_norm_backward(dy: torch.Tensor, saved: LayerNormSaved, layout: int, sh
     dev = _lead("dy", dy, 3)
     dt, B = dy.dtype, sh.B
     mixed = layout == A.TM_LAYOUT_MIXED
+    if residual_is_x and not mixed:
+        raise ValueError("residual_is_x is the mixed layout's: in the row layout both gradients are dx")
     if mixed:
         banks, width = sh.H, sh.T * sh.D // max(sh.H, 1)
         xshape, rows = (B, sh.T, sh.D), (B, banks, width)
@@ -1038,15 +1040,14 @@ def layer_norm_backward(dy: torch.Tensor, saved: LayerNormSaved, layout: int, sh
     mean = _arg("saved statistics", saved.stats, (2, B, banks), torch.float32, dev)
     if dx is None:
         dx = torch.empty_like(dy) if xshape == rows else dy.new_empty(xshape)
-    self_ = residual_is_x and mixed
-    dres = dy.new_empty(rows) if mixed and saved.residual and not self_ else None
+    dres = dy.new_empty(rows) if mixed and saved.residual and not residual_is_x else None
     dgain, dbias = dy.new_empty(width), dy.new_empty(width)
     lib_ = A.load()
     w = A.tm_layer_norm_w(banks, width, _arg("gain", gain, (width,), dt, dev), None)
     n = lib_.tm_layer_norm_backward_workspace_bytes(sh, layout, w)
     ws = _ws(n, dy.device, workspace)
     st = lib_.tm_layer_norm_backward(
-        px, pres, ck, mean, mean + 4 * B * banks, pdy, layout, sh, w, 1 if self_ else 0, _arg("dx", dx, xshape, dt, dev),
+        px, pres, ck, mean, mean + 4 * B * banks, pdy, layout, sh, w, 1 if residual_is_x else 0, _arg("dx", dx, xshape, dt, dev),
         None if dres is None else dres.data_ptr(), A.tm_layer_norm_grads(dgain.data_ptr(), dbias.data_ptr()), _p(ws),
         ws.numel(), _stream_of(None, dev))
     if st:

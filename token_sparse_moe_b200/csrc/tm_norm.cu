@@ -1032,10 +1032,11 @@ static cudaError_t launch_ln_self_t(const NormParams& p, int sms, int* nblk, cud
 }
 
 // ---- sample kernels (X the residual too)
-// bytes of a padded token row (piece: bytes of dh columns; a multiple of 16)
+// bytes of a padded token row of `bytes` (a multiple of 16, as the bulk copies into it need, whose every row
+// starts at a multiple of this); piece: bytes of dh columns
 static uint32_t sample_ld(uint32_t bytes, uint32_t piece) {
-    if (piece < 16) piece = 16;
-    return bytes + (piece + 128 - bytes % 128) % 128;
+    piece = (piece + 15) & ~15u;
+    return bytes + (piece % 128 + 128 - bytes % 128) % 128;
 }
 // Slots of the forward's ring, 4 at most (0: none fits): as many blocks an SM, up to 3, as leave each two
 // slots, so that loads run ahead.
@@ -1134,7 +1135,8 @@ cudaError_t launch_ln_bwd(int dtype, const NormParams& p, bool self, void* dgain
         const int esz = dtype == 1 ? 2 : 4;
         const bool vec = norm_vec(dtype, p.map.W);
         const uint32_t ld = sample_ld(p.map.W * esz, p.map.dh * esz), ldc = sample_ld(p.map.W, p.map.dh);
-        const bool sample = self && (size_t)p.map.banks * p.map.W * esz >= kSampleLeast && (!ck || p.map.W % 16 == 0) &&
+        const bool sample = self && (size_t)p.map.banks * p.map.W * esz >= kSampleLeast &&
+                            (!ck || (p.map.W % 16 == 0 && ldc <= ld)) &&
                             sample_bwd_smem(p.map.banks, p.map.W, ld) <= kSampleSmem;
 #define X(FN, ...)                                                                                            \
     e = dtype == 1 ? (ck ? FN<__nv_bfloat16, true>(__VA_ARGS__) : FN<__nv_bfloat16, false>(__VA_ARGS__))      \
