@@ -139,6 +139,18 @@ def test_layer_norm_mixed(dtype, B, T, D, H, ckpt):
         check("dbias", grads["dbias"], b["dbias"], tb)
 
 
+# (enough samples that several share a slot of shared memory, the last slot not full; odd and single heads)
+MANY = [(1185, 16, 512, 16), (1301, 16, 256, 16), (1789, 8, 128, 8), (2501, 13, 104, 13), (6001, 4, 32, 4),
+        (1207, 2, 128, 2), (20011, 3, 48, 3), (40009, 1, 16, 1)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,D,H", MANY)
+@pytest.mark.parametrize("ckpt", [False, True])
+def test_layer_norm_of_many_small_samples(dtype, B, T, D, H, ckpt):
+    test_layer_norm_mixed(dtype, B, T, D, H, ckpt)
+
+
 # ------------------------------------------------------------------ per-token linear layer
 LINEAR = [(1, 1, 8, 8), (1, 3, 64, 128), (5, 2, 72, 40), (64, 2, 64, 64), (128, 1, 256, 256), (129, 2, 128, 264),
           (200, 3, 136, 328), (300, 2, 320, 96), (33, 1, 768, 1536), (1000, 1, 40, 72), (700, 2, 384, 520)]

@@ -358,7 +358,6 @@ __device__ __forceinline__ void zero_sums(float2 (&dg)[NV][Pairs<V>::N], float2 
 // time; sm holds room * W floats and is free when this is called.
 template <int V, int NV, int G>
 __device__ __forceinline__ void ln_store_partials(const NormParams& p, float* sm, int room, int groups, int grp, int gl,
-                                                  int c0, int c1,
                                                   const float2 (&dg)[NV][Pairs<V>::N],
                                                   const float2 (&db)[NV][Pairs<V>::N]) {
     const int W = p.map.W;
@@ -369,8 +368,8 @@ __device__ __forceinline__ void ln_store_partials(const NormParams& p, float* sm
             if (grp >= g0 && grp < g0 + room) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int c = c0 + (gl + G * i) * V;
-                    if (c < c1) {
+                    const int c = (gl + G * i) * V;
+                    if (c < W) {
                         float* o = sm + (grp - g0) * W + c;
 #pragma unroll
                         for (int k = 0; k < Pairs<V>::N; ++k) {
@@ -440,7 +439,7 @@ __global__ void __launch_bounds__(NormBlock<G>::THREADS) ln_bwd_kernel(const Nor
             if (mixed && p.dres) Pack<T, V>::store((T*)p.dres + (size_t)a.row * W + c, d);
         });
     }
-    if (p.part) ln_store_partials<V, NV, G>(p, nsm + W, ROWS, ROWS, threadIdx.x / G, gl, 0, W, dg, db);
+    if (p.part) ln_store_partials<V, NV, G>(p, nsm + W, ROWS, ROWS, threadIdx.x / G, gl, dg, db);
 }
 
 // Backward of LN(Mix(X) + X) (T = H, W = D) for samples that the ring of ln_sample_bwd_kernel does not take:
@@ -488,7 +487,7 @@ __global__ void __launch_bounds__(THREADS) ln_bwd_self_kernel(const NormParams p
         }
         __syncthreads();
     }
-    if (p.part) ln_store_partials<V, NV, 32>(p, sm, min(H, THREADS / 32), THREADS / 32, warp, lane, 0, W, dg, db);
+    if (p.part) ln_store_partials<V, NV, 32>(p, sm, min(H, THREADS / 32), THREADS / 32, warp, lane, dg, db);
 }
 
 // ------------------------------------------------------------------ whole samples: LN(Mix(X) + X)
@@ -497,7 +496,15 @@ __global__ void __launch_bounds__(THREADS) ln_bwd_self_kernel(const NormParams p
 // slots ahead of the arithmetic, so that the scattered reads of the Mix view (pieces of dh columns, one
 // per token) cost shared-memory cycles instead of L1 lookups, and loads stay in flight while rows are
 // worked on.  A token row of a slot is `ld` bytes, padded so that ld = dh * esz modulo 128: the pieces
-// of 8 lanes then fall into different banks.
+// of 8 lanes then fall into different banks.  A slot takes `per_slot` samples (the last of a tensor fewer):
+// what a slot costs besides its rows -- waits, barriers, the latency of its first loads -- is paid once for all.
+struct SampleGeo {
+    uint32_t ld;               // bytes of a padded token row, and
+    uint32_t ldc;              // of a padded row of the checkpoint's codes (the backward's)
+    int nb;                    // slots (the forward's)
+    int per_slot, nslots;      // samples a slot, and slots' worth of samples in the tensor
+    FastDiv heads;             // rows a sample
+};
 struct SampleRing {
     uint8_t* base;             // slots
     uint64_t* full;            // one barrier each
@@ -505,7 +512,7 @@ struct SampleRing {
     int nb;
 };
 
-// Token rows of one sample (rows x bytes each, contiguous in memory) into a slot, by one warp.
+// Token rows of a slot's samples (rows x bytes each, contiguous in memory), by one warp.
 __device__ __forceinline__ void sample_load(const SampleRing& r, int slot, const void* src, int rows, uint32_t bytes,
                                             uint32_t ld) {
     uint64_t* bar = r.full + slot;
@@ -533,13 +540,14 @@ constexpr int sample_warps(int nv) { return nv <= 2 ? 8 : 24; }
 // Dynamic shared memory: nb slots, then gain and bias.
 template <typename T, int V, int NV, int NW>
 __global__ void __launch_bounds__(NW * 32 + 32, NV <= 2 ? 3 : 1)
-    ln_sample_fwd_kernel(const NormParams p, uint32_t ld, int nb) {
+    ln_sample_fwd_kernel(const NormParams p, const SampleGeo geo) {
     extern __shared__ __align__(128) uint8_t sms[];
     __shared__ uint64_t bars[8];               // [slot] loaded, [4 + slot] read by every warp
     constexpr int NP = Pairs<V>::N, ES = sizeof(T);
     const int W = p.map.W, H = p.map.banks, dh = p.map.dh;
-    const uint32_t bytes = W * ES;
-    const SampleRing ring{sms, bars, H * ld, nb};
+    const uint32_t bytes = W * ES, ld = geo.ld;
+    const int nb = geo.nb, all = geo.per_slot * H;
+    const SampleRing ring{sms, bars, all * ld, nb};
     float* sg = reinterpret_cast<float*>(sms + (size_t)nb * ring.slot_bytes);
     float* sb = sg + W;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -552,15 +560,20 @@ __global__ void __launch_bounds__(NW * 32 + 32, NV <= 2 ? 3 : 1)
         fence_barrier_init();
     }
     __syncthreads();
-    const size_t per = (size_t)H * W;
-    // sample i of this block is blockIdx.x + i * gridDim.x, in slot i % nb
-    const int mine = blockIdx.x < p.B ? (p.B - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+    // group i of samples of this block is blockIdx.x + i * gridDim.x, in slot i % nb
+    const int mine = blockIdx.x < geo.nslots ? (geo.nslots - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+    auto first_row = [&](int i) { return (blockIdx.x + i * (int)gridDim.x) * all; };
+    auto rows_of = [&](int i) { return min(all, p.B * H - first_row(i)); };
+    auto load = [&](int i, int slot) {
+        const int r0 = first_row(i);
+        sample_load(ring, slot, (const T*)p.x + (size_t)r0 * W, rows_of(i), bytes, ld);
+    };
     if (warp == NW) {
         int slot = 0, i = 0;
         uint32_t ph = 0;
         for (; i < mine; ++i) {
             if (i >= nb && !warp_wait(&bars[4 + slot], ph ^ 1, 0x815)) break;
-            sample_load(ring, slot, (const T*)p.x + (blockIdx.x + (size_t)i * gridDim.x) * per, H, bytes, ld);
+            load(i, slot);
             if (++slot == nb) { slot = 0; ph ^= 1; }
             if (i == 0) break;                 // the first on its way, then the vectors of all rows
         }
@@ -569,7 +582,7 @@ __global__ void __launch_bounds__(NW * 32 + 32, NV <= 2 ? 3 : 1)
         __syncthreads();
         for (++i; i < mine; ++i) {
             if (i >= nb && !warp_wait(&bars[4 + slot], ph ^ 1, 0x815)) break;
-            sample_load(ring, slot, (const T*)p.x + (blockIdx.x + (size_t)i * gridDim.x) * per, H, bytes, ld);
+            load(i, slot);
             if (++slot == nb) { slot = 0; ph ^= 1; }
         }
         if (i < mine)                          // given up: the loads in flight land before the block ends
@@ -596,26 +609,28 @@ __global__ void __launch_bounds__(NW * 32 + 32, NV <= 2 ? 3 : 1)
     for (int done = 0; done < mine; ++done) {
         if (!warp_wait(&bars[slot], ph, 0x810)) break;
         const uint8_t* sx = sms + slot * ring.slot_bytes;
-        const int b = blockIdx.x + done * gridDim.x;
-        for (int h = warp; h < H; h += NW) {
+        const int r0 = first_row(done), rows = rows_of(done);
+        for (int r = warp; r < rows; r += NW) {
+            const int s0 = geo.heads.div(r) * H;             // the sample's first row, head r - s0
+            const uint8_t* mx = sx + s0 * ld + (r - s0) * dh * ES;
             float2 z[NV][NP];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (lane + 32 * i) * V;
-                Pack<T, V> a, r;
+                Pack<T, V> a, w;
                 a.zero();
-                r.zero();
+                w.zero();
                 if (c < W) {
-                    a.load_shared(sx + moff[i] + h * dh * ES);
-                    r.load_shared(sx + h * ld + c * ES);
+                    a.load_shared(mx + moff[i]);
+                    w.load_shared(sx + r * ld + c * ES);
                 }
                 float2 rv[NP];
                 a.get(z[i]);
-                r.get(rv);
+                w.get(rv);
 #pragma unroll
                 for (int k = 0; k < NP; ++k) z[i][k] = add2(z[i][k], rv[k]);
             }
-            ln_fwd_row<T, V, NV, 32>(p, z, true, b * H + h, lane, sg, sb, nullptr, turn);
+            ln_fwd_row<T, V, NV, 32>(p, z, true, r0 + r, lane, sg, sb, nullptr, turn);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[4 + slot]);
@@ -626,28 +641,28 @@ __global__ void __launch_bounds__(NW * 32 + 32, NV <= 2 ? 3 : 1)
 // Backward of the same, dX = dz + Revert(dz).  Mix(X) + X is symmetric under exchange of a token and a
 // head (its element (row h, column t * dh + j) is X[t][h * dh + j] + X[h][t * dh + j]), and so is dX:
 // dX[t][h * dh + j] = dz[t][h * dh + j] + dz[h][t * dh + j] = dX[h][t * dh + j].  First a sample's row
-// means, with dgain and dbias on the way, a warp a row (or one of PARTS parts of it, so that the sums fit
-// the registers of 24 warps); then every pair of elements once: dz is never stored.  Three slots: X (or the
+// means, with dgain and dbias on the way, a warp a row; then every pair of elements once: dz is never stored.  Three slots: X (or the
 // checkpoint's codes) of this sample and of the next, and dy.  The second step reads dy again through the
 // L2, where the first's copy has just come from, so that the next dy is on its way meanwhile: with dy kept
 // in its slot to the end, two samples of 73 KB do not fit, and a third of the time went by waiting for the
 // next one.  Every warp issues some of a sample's row copies (all of them take one warp some 4000 cycles).
-// VA: vector of the first step (parts of W / PARTS columns), NVA of them a lane.
-// Dynamic shared memory: 3 slots, gain, [H] row constants, [H] statistics, [PARTS][H] sums.
-template <typename T, int VA, int NVA, int PARTS, bool CK, int NW>
-__global__ void __launch_bounds__(NW * 32, NW <= 8 ? 2 : 1)
-    ln_sample_bwd_kernel(const NormParams p, uint32_t ld, uint32_t ldc) {
+// Dynamic shared memory: 3 slots, gain, and per row of a slot its constants, statistics and sums.
+template <typename T, int NV, bool CK, int NW>
+__global__ void __launch_bounds__(NW * 32, NW <= 12 ? 2 : 1)
+    ln_sample_bwd_kernel(const NormParams p, const SampleGeo geo) {
     extern __shared__ __align__(128) uint8_t sms[];
     __shared__ uint64_t bars[3];       // loaded: X slots 0 and 1, dy
-    constexpr int V = sizeof(T) == 2 ? 8 : 4, NP = Pairs<V>::N, NPA = Pairs<VA>::N, ES = sizeof(T);
+    constexpr int V = sizeof(T) == 2 ? 8 : 4, NP = Pairs<V>::N, ES = sizeof(T);
     const int W = p.map.W, H = p.map.banks, dh = p.map.dh;
     const int nblk = (W + kCk8Block - 1) / kCk8Block;
-    const uint32_t bytes = W * ES;
-    const SampleRing ring{sms, bars, H * ld, 3};
+    const uint32_t bytes = W * ES, ld = geo.ld, ldc = geo.ldc;
+    constexpr bool MULTI = NV <= 2;    // wider rows: one sample a slot, which spares the registers of its walk
+    const int all = MULTI ? geo.per_slot * H : H;
+    const SampleRing ring{sms, bars, all * ld, 3};
     float* sg = reinterpret_cast<float*>(sms + (size_t)3 * ring.slot_bytes);
     float4* rowc = reinterpret_cast<float4*>(sg + W);      // {rs, mu, -rs m1, -rs^2 m2}
-    float2* rowstat = reinterpret_cast<float2*>(rowc + H); // {mu, rs}
-    float2* rowsum = rowstat + H;                          // [PARTS][H] sums of dn and dn n
+    float2* rowstat = reinterpret_cast<float2*>(rowc + all); // {mu, rs}
+    float2* rowsum = rowstat + all;                          // sums of dn and dn n
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int turn = 0;
     if (threadIdx.x == 0) {
@@ -655,48 +670,52 @@ __global__ void __launch_bounds__(NW * 32, NW <= 8 ? 2 : 1)
         fence_barrier_init();
     }
     __syncthreads();
-    const size_t per = (size_t)H * W;
-    const int mine = blockIdx.x < p.B ? (p.B - 1 - blockIdx.x) / gridDim.x + 1 : 0;
-    float2 dg[NVA][NPA], db[NVA][NPA];
-    zero_sums<VA, NVA>(dg, db);
-    const int part = warp % PARTS, c0 = part * (W / PARTS), c1 = c0 + W / PARTS;
-    // this block's i-th sample, row copies dealt out to the warps: X or codes into slot i % 2, dy into slot 2
-    auto load = [&](int slot, const void* src, uint32_t row_bytes, uint32_t row_ld) {
-        if (threadIdx.x == 0) mbar_arrive_expect_tx(&bars[slot], H * row_bytes);
+    const int mine = blockIdx.x < geo.nslots ? (geo.nslots - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+    auto first_row = [&](int i) { return (blockIdx.x + i * (int)gridDim.x) * all; };
+    auto rows_of = [&](int i) { return MULTI ? min(all, p.B * H - first_row(i)) : all; };
+    float2 dg[NV][NP], db[NV][NP];
+    zero_sums<V, NV>(dg, db);
+    // this block's i-th group of samples, row copies dealt out to the warps: X or codes into slot i % 2, dy into
+    // slot 2
+    auto load = [&](int i, int slot, const void* src, uint32_t row_bytes, uint32_t row_ld) {
+        const int rows = rows_of(i);
+        src = (const uint8_t*)src + (size_t)first_row(i) * row_bytes;
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(&bars[slot], rows * row_bytes);
         uint8_t* dst = sms + slot * ring.slot_bytes;
-        for (int t = lane * NW + warp; t < H; t += 32 * NW)
+        for (int t = lane * NW + warp; t < rows; t += 32 * NW)
             bulk_load(dst + t * row_ld, (const uint8_t*)src + (size_t)t * row_bytes, row_bytes, &bars[slot]);
     };
     auto load_x = [&](int i) {
-        const size_t b = blockIdx.x + (size_t)i * gridDim.x;
-        if (CK) load(i & 1, p.codes + b * per, W, ldc);
-        else load(i & 1, (const T*)p.x + b * per, bytes, ld);
+        if (CK) load(i, i & 1, p.codes, W, ldc);
+        else load(i, i & 1, p.x, bytes, ld);
     };
-    auto load_d = [&](int i) { load(2, (const T*)p.dy + (blockIdx.x + (size_t)i * gridDim.x) * per, bytes, ld); };
+    auto load_d = [&](int i) { load(i, 2, p.dy, bytes, ld); };
     if (mine > 0) {
         load_x(0);
         load_d(0);
     }
     stage_vec<T, V>(sg, p.gain, W, 1.f);
-    int moff[NVA];
+    int moff[NV];
 #pragma unroll
-    for (int i = 0; i < NVA; ++i) {
-        const int c = c0 + (lane + 32 * i) * VA, t = c / dh;
+    for (int i = 0; i < NV; ++i) {
+        const int c = (lane + 32 * i) * V, t = c / dh;
         moff[i] = t * (int)ld + (c - t * dh) * ES;
     }
-    // the second step's vectors: (H + 1) / 2 folded rows of H + 1 pieces of vpd vectors; this thread's
-    // first and the step to its next
+    // the second step's vectors: per sample (H + 1) / 2 folded rows of H + 1 pieces of vpd vectors; this
+    // thread's first and the step to its next
     constexpr int TH = NW * 32;
-    const int vpd = dh / V, npair = (H + 1) / 2 * (H + 1) * vpd;
-    const int j0 = threadIdx.x % vpd, k0 = threadIdx.x / vpd % (H + 1), i0 = threadIdx.x / vpd / (H + 1);
-    const int dj = TH % vpd, dk = TH / vpd % (H + 1), di = TH / vpd / (H + 1);
-    // thread h < H holds row h's statistics a sample ahead (H <= 256 = the smallest block: W >= 4 H)
+    const int vpd = dh / V, folds = (H + 1) / 2, npair = folds * (H + 1) * vpd;
+    // (vector of a piece, piece and folded row in 10 bits each, as registers are short here)
+    auto walk = [&](int v) { return v % vpd | v / vpd % (H + 1) << 10 | v / vpd / (H + 1) % folds << 20; };
+    const int jki0 = walk(threadIdx.x), djki = walk(TH);
+    const int s0 = MULTI ? threadIdx.x / npair * H : 0, ds = MULTI ? TH / npair * H : 0;
+    // thread r holds row r's statistics a group ahead (a slot has at most 256 rows, the smallest block's threads)
     float2 stat = make_float2(0.f, 0.f);
-    auto fetch_stat = [&](int b) {
-        if (threadIdx.x < H)
-            stat = make_float2(__ldg(p.mean + (size_t)b * H + threadIdx.x), __ldg(p.rstd + (size_t)b * H + threadIdx.x));
+    auto fetch_stat = [&](int i) {
+        const int r = first_row(i) + threadIdx.x;
+        if (threadIdx.x < rows_of(i)) stat = make_float2(__ldg(p.mean + r), __ldg(p.rstd + r));
     };
-    if (mine > 0) fetch_stat(blockIdx.x);
+    if (mine > 0) fetch_stat(0);
     __syncthreads();
     int done = 0;
     for (; done < mine; ++done) {
@@ -704,48 +723,44 @@ __global__ void __launch_bounds__(NW * 32, NW <= 8 ? 2 : 1)
         // one warp waits for the data, the others at the barrier; it also says that every warp is done with
         // the last sample, its slot of X and its row constants
         const bool ok = warp != 0 || (warp_wait(&bars[done & 1], phx, 0x812) && warp_wait(&bars[2], phd, 0x813));
-        if (threadIdx.x < H) rowstat[threadIdx.x] = stat;
+        if (threadIdx.x < all) rowstat[threadIdx.x] = stat;
         if (!__syncthreads_and(ok)) break;
         mbar_try_wait(&bars[done & 1], phx);           // complete: each thread sees it for itself
         mbar_try_wait(&bars[2], phd);
         if (done + 1 < mine) load_x(done + 1);
         const uint8_t* sx = sms + (done & 1) * ring.slot_bytes;
         const uint8_t* sd = sms + 2 * ring.slot_bytes;
-        const int b = blockIdx.x + done * gridDim.x;
-        const int8_t* ex = CK ? p.exps + (size_t)b * H * nblk : nullptr;
-        for (int h = warp / PARTS; h < H; h += NW / PARTS) {
-            const float2 st = rowstat[h];
+        const int r0 = first_row(done), rows = rows_of(done);
+        const int8_t* ex = CK ? p.exps + (size_t)r0 * nblk : nullptr;
+        for (int r = warp; r < rows; r += NW) {
+            const int sr = MULTI ? geo.heads.div(r) * H : 0; // the sample's first row, head r - sr
+            const uint8_t* mx = sx + sr * ld + (r - sr) * dh * ES;
+            const float2 st = rowstat[r];
             float2 s1 = make_float2(0.f, 0.f), s2 = s1;
 #pragma unroll
-            for (int i = 0; i < NVA; ++i) {
-                const int c = c0 + (lane + 32 * i) * VA;
-                if (c < c1) {
-                    float2 n[NPA], d[NPA], g[NPA];
-                    Pack<T, VA> w;
+            for (int i = 0; i < NV; ++i) {
+                const int c = (lane + 32 * i) * V;
+                if (c < W) {
+                    float2 n[NP], d[NP], g[NP];
+                    Pack<T, V> w;
                     if constexpr (CK) {
-                        uint32_t q[(VA + 3) / 4];
-                        ck8_load_shared<VA>(sx + h * ldc + c, q);
-                        ck8_values<VA>(q, ck8_scale(__ldg(ex + h * nblk + c / kCk8Block)), n);
+                        uint32_t q[(V + 3) / 4];
+                        ck8_load_shared<V>(sx + r * ldc + c, q);
+                        ck8_values<V>(q, ck8_scale(__ldg(ex + r * nblk + c / kCk8Block)), n);
                     } else {
-                        float2 r[NPA];
-                        w.load_shared(sx + moff[i] + h * dh * ES);
+                        float2 x[NP];
+                        w.load_shared(mx + moff[i]);
                         w.get(n);
-                        w.load_shared(sx + h * ld + c * ES);
-                        w.get(r);
+                        w.load_shared(sx + r * ld + c * ES);
+                        w.get(x);
 #pragma unroll
-                        for (int k = 0; k < NPA; ++k) n[k] = add2(n[k], r[k]);
+                        for (int k = 0; k < NP; ++k) n[k] = add2(n[k], x[k]);
                     }
-                    w.load_shared(sd + h * ld + c * ES);
+                    w.load_shared(sd + r * ld + c * ES);
                     w.get(d);
-                    if constexpr (VA == V) {
-                        staged<V>(sg, W, c, g);
-                    } else {                           // half a vector of the staged layout
-                        const float4 a = *reinterpret_cast<const float4*>(sg + (c & 4 ? W / 2 : 0) + (c >> 3) * 4);
-                        g[0] = make_float2(a.x, a.y);
-                        g[NPA - 1] = make_float2(a.z, a.w);
-                    }
+                    staged<V>(sg, W, c, g);
 #pragma unroll
-                    for (int k = 0; k < NPA; ++k) {
+                    for (int k = 0; k < NP; ++k) {
                         n[k] = mul2(add2(n[k], f2(-st.x)), f2(st.y));
                         dg[i][k] = fma2(d[k], n[k], dg[i][k]);
                         db[i][k] = add2(db[i][k], d[k]);
@@ -756,45 +771,52 @@ __global__ void __launch_bounds__(NW * 32, NW <= 8 ? 2 : 1)
                 }
             }
             const float2 m = row_sum2<32>(make_float2(s1.x + s1.y, s2.x + s2.y), nullptr, turn);
-            if (lane == 0) rowsum[part * H + h] = m;
+            if (lane == 0) rowsum[r] = m;
         }
-        if (done + 1 < mine) fetch_stat(b + gridDim.x);
+        if (done + 1 < mine) fetch_stat(done + 1);
         // the second step's pairs (t <= h): rows i and H-1-i of the triangle together are H + 1 pieces; the
         // first two vectors of dy are on their way before the barriers, then always the next two
-        T* out = (T*)p.dx + (size_t)b * per;
-        const T* dyb = (const T*)p.dy + (size_t)b * per;
-        // piece k of folded row i, vector j of it: advanced by TH with carries
-        int j = j0, k = k0, i = i0, u = threadIdx.x;
+        const int nvec = MULTI ? rows / H * npair : npair;
+        T* out = (T*)p.dx + (size_t)r0 * W;
+        const T* dyb = (const T*)p.dy + (size_t)r0 * W;
+        // piece k of folded row i of the sample whose first row is s, vector j of it: advanced by TH with carries
+        int jki = jki0, s = s0, left = nvec - threadIdx.x;
         struct Pair {
-            int t, h, j;                        // t < 0: none
+            uint32_t rows, cols;                // t | h << 16, rows of the slot, and their columns; none: cols = ~0
         };
         Pair q[2];
         Pack<T, V> wa[2], wb[2];
         auto fetch = [&](int at) {
+            const int j = jki & 1023, k = jki >> 10 & 1023, i = jki >> 20;
             const bool low = k >= H - i;
+            const int t = low ? H - 1 - i : i;
+            const int h = low ? k - 1 : i + k;  // t + k - (H - i), or i + k
             Pair& c = q[at];
-            c.t = low ? H - 1 - i : i;
-            c.h = low ? k - 1 : i + k;          // t + k - (H - i), or i + k
-            c.j = j * V;
-            if (u >= npair || (low && c.t == i)) c.t = -1;     // odd H: the middle row is its own partner
-            if (c.t >= 0) {
-                wa[at].load(dyb + (c.t * W + c.h * dh + c.j));
-                wb[at].load(dyb + (c.h * W + c.t * dh + c.j));
+            if (left <= 0 || (low && t == i)) { // odd H: the middle row is its own partner
+                c.cols = ~0u;
+            } else {
+                const int ct = h * dh + j * V, ch = t * dh + j * V;
+                c.rows = (s + t) | (s + h) << 16;
+                c.cols = ct | ch << 16;
+                wa[at].load(dyb + ((s + t) * W + ct));
+                wb[at].load(dyb + ((s + h) * W + ch));
             }
-            u += TH;
-            j += dj;
-            k += dk;
-            i += di;
-            if (j >= vpd) { j -= vpd; ++k; }
-            if (k > H) { k -= H + 1; ++i; }
+            left -= TH;
+            jki += djki;
+            if (MULTI) s += ds;
+            if ((jki & 1023) >= vpd) jki += (1 << 10) - vpd;
+            if ((jki >> 10 & 1023) > H) jki += (1 << 20) - ((H + 1) << 10);
+            if (MULTI && (jki >> 20) >= folds) {
+                jki -= folds << 20;
+                s += H;
+            }
         };
         fetch(0);
         fetch(1);
         __syncthreads();
         if (done + 1 < mine) load_d(done + 1);
-        if (threadIdx.x < H) {
-            float2 m = rowsum[threadIdx.x];
-            if (PARTS == 2) m = add2(m, rowsum[H + threadIdx.x]);
+        if (threadIdx.x < rows) {
+            const float2 m = rowsum[threadIdx.x];
             const float2 st = rowstat[threadIdx.x];
             rowc[threadIdx.x] = make_float4(st.y, st.x, -st.y * (m.x * p.inv_w), -st.y * st.y * (m.y * p.inv_w));
         }
@@ -811,23 +833,23 @@ __global__ void __launch_bounds__(NW * 32, NW <= 8 ? 2 : 1)
             wa[at].get(da);
             wb[at].get(dd);
             fetch(at);
-            if (c.t < 0) return;
-            const int ca = c.h * dh + c.j, cb = c.t * dh + c.j;
+            if (c.cols == ~0u) return;
+            const int rt = c.rows & 0xffff, rh = c.rows >> 16, ct = c.cols & 0xffff, ch = c.cols >> 16;
             if constexpr (CK) {
-                codes(c.t, ca, za);
-                codes(c.h, cb, zb);
+                codes(rt, ct, za);
+                codes(rh, ch, zb);
             } else {
                 Pack<T, V> w;
-                w.load_shared(sx + c.t * ld + ca * ES);
+                w.load_shared(sx + rt * ld + ct * ES);
                 w.get(za);
-                w.load_shared(sx + c.h * ld + cb * ES);
+                w.load_shared(sx + rh * ld + ch * ES);
                 w.get(zb);
 #pragma unroll
                 for (int e = 0; e < NP; ++e) za[e] = add2(za[e], zb[e]);
             }
-            staged<V>(sg, W, ca, ga);
-            staged<V>(sg, W, cb, gb);
-            const float4 ra = rowc[c.t], rb = rowc[c.h];
+            staged<V>(sg, W, ct, ga);
+            staged<V>(sg, W, ch, gb);
+            const float4 ra = rowc[rt], rb = rowc[rh];
             float2 o[NP];
             if constexpr (CK) {
 #pragma unroll
@@ -844,16 +866,16 @@ __global__ void __launch_bounds__(NW * 32, NW <= 8 ? 2 : 1)
                     o[e] = fma2(mul2(da[e], ga[e]), f2(ra.x),
                                 fma2(mul2(dd[e], gb[e]), f2(rb.x), fma2(add2(za[e], f2(-ra.y)), wz, cz)));
             }
-            Pack<T, V>::store(out + (c.t * W + ca), o);
-            if (c.t != c.h) Pack<T, V>::store(out + (c.h * W + cb), o);
+            Pack<T, V>::store(out + (rt * W + ct), o);
+            if (rt != rh) Pack<T, V>::store(out + (rh * W + ch), o);
         };
-        for (int v = threadIdx.x; v < npair; v += 2 * TH) {
+        for (int v = threadIdx.x; v < nvec; v += 2 * TH) {
             step(0);
-            if (v + TH < npair) step(1);
+            if (v + TH < nvec) step(1);
         }
     }
     if (done < mine) {
-        // given up, before anything of this sample was started: the loads in flight are its own two
+        // given up, before anything of this group was started: the loads in flight are its own two
         if (threadIdx.x == 0) {
             mbar_wait(&bars[done & 1], (done >> 1) & 1, 0x814);
             mbar_wait(&bars[2], done & 1, 0x816);
@@ -862,8 +884,7 @@ __global__ void __launch_bounds__(NW * 32, NW <= 8 ? 2 : 1)
     }
     if (p.part) {                                // (its first barrier is behind every read of the slots)
         const int fit = (int)((size_t)3 * ring.slot_bytes / (W * sizeof(float)));
-        ln_store_partials<VA, NVA, 32>(p, reinterpret_cast<float*>(sms), min(fit, NW / PARTS), NW / PARTS,
-                                       warp / PARTS, lane, c0, c1, dg, db);
+        ln_store_partials<V, NV, 32>(p, reinterpret_cast<float*>(sms), min(fit, NW), NW, warp, lane, dg, db);
     }
 }
 
@@ -1005,6 +1026,12 @@ static cudaError_t launch_ln_bwd_t(const NormParams& p, bool vec, int sms, int* 
 constexpr int kSelfThreads = 512;
 constexpr size_t kSelfSmem = 220 * 1024;     // of a sample in fp32; the gain comes on top
 constexpr size_t kSampleSmem = 226 * 1024;
+// The forward's samples of at least 8 KB (which makes rows of 181 or more values): smaller ones have narrow
+// rows, of which the row kernel works on several a warp.  300 MB of bf16, sample / row kernel: 48 x 768 112 /
+// 119 us, 16 x 512 102 / 107, 16 x 256 126 / 137, 8 x 256 126 / 131, 13 x 104 300 / 157, 8 x 128 240 / 134.
+// (The backward's samples may be of any size: dX needs the sample's other rows, and the fallback that keeps dz
+// in shared memory as fp32 takes 689 us for 48 x 768 and 904 for 8 x 128 where this one takes 234 and 376.)
+constexpr size_t kSampleLeast = 8 * 1024;
 
 // The sample of LN(Mix(X) + X)'s backward has to fit the shared memory as fp32, a row one warp.
 bool ln_self_supported(int H, int W) { return (size_t)H * W * 4 <= kSelfSmem && W <= 1024; }
@@ -1038,67 +1065,91 @@ static uint32_t sample_ld(uint32_t bytes, uint32_t piece) {
     piece = (piece + 15) & ~15u;
     return bytes + (piece % 128 + 128 - bytes % 128) % 128;
 }
+// Dynamic shared memory of each of `blocks` blocks on an SM: 228 KB less 1 KB a block for the system and 1 KB
+// for the kernels' own static part.
+static size_t sample_room(int blocks) { return blocks == 1 ? kSampleSmem : (228 * 1024) / blocks - 2048; }
+static size_t sample_bwd_smem(int rows, int W, uint32_t ld) {
+    return (size_t)3 * rows * ld + W * sizeof(float) + rows * (sizeof(float4) + 2 * sizeof(float2));
+}
+// Samples of a slot: as many as let two of the backward's blocks share an SM (some 32 KB; backward of 300 MB
+// of bf16 in samples of 8 x 256: 476 us one by one, 260 in 16 KB, 229 in 32 KB), where there are enough for
+// every block to take two slots; never more than 256 rows.
+static int samples_per_slot(int B, int H, int W, uint32_t ld, int sms) {
+    const size_t fixed = sample_bwd_smem(0, W, ld), each = sample_bwd_smem(H, W, ld) - fixed;
+    size_t n = (sample_room(2) - fixed) / each;
+    if (n > (size_t)256 / H) n = 256 / H;
+    if (n > (size_t)B / (4 * sms)) n = B / (4 * sms);
+    return n > 1 ? (int)n : 1;
+}
+// The kernels' geometry for H rows of W values of esz bytes a sample.
+static SampleGeo sample_geo(int B, int H, int W, int dh, int esz, int sms) {
+    const bool wide = W > 64 * (16 / esz);
+    SampleGeo g;
+    g.ld = sample_ld(W * esz, dh * esz);
+    g.ldc = sample_ld(W, dh);
+    g.nb = 0;
+    g.per_slot = wide ? 1 : samples_per_slot(B, H, W, g.ld, sms);
+    g.nslots = (B + g.per_slot - 1) / g.per_slot;
+    g.heads = fast_div(H);
+    return g;
+}
 // Slots of the forward's ring, 4 at most (0: none fits): as many blocks an SM, up to 3, as leave each two
 // slots, so that loads run ahead.
 static int sample_slots(size_t slot, size_t extra) {
     for (int blocks = 3; blocks >= 1; --blocks) {
-        const size_t room = blocks == 1 ? kSampleSmem : (227 * 1024) / blocks - 1024;
+        const size_t room = sample_room(blocks);
         if (room <= extra) continue;
         const int nb = (int)((room - extra) / slot);
         if (nb >= 2 || (blocks == 1 && nb >= 1)) return nb > 4 ? 4 : nb;
     }
     return 0;
 }
-// Samples of at least 8 KB; smaller ones leave a block's threads idle, and the row kernels take them.
-constexpr size_t kSampleLeast = 8 * 1024;
 
 template <typename T, int V, int NV>
-static cudaError_t launch_sample_fwd(const NormParams& p, uint32_t ld, int nb, int sms, cudaStream_t st) {
+static cudaError_t launch_sample_fwd(const NormParams& p, const SampleGeo& g, int sms, cudaStream_t st) {
     constexpr int NW = sample_warps(NV), THREADS = NW * 32 + 32;
     auto kern = ln_sample_fwd_kernel<T, V, NV, NW>;
     static std::atomic<int> cache[64];
     int per_sm = 0;
     cudaError_t e = norm_resident(kern, THREADS, kSampleSmem, cache, &per_sm);
     if (e != cudaSuccess) return e;
-    const size_t smem = (size_t)nb * p.map.banks * ld + 2 * p.map.W * sizeof(float);
-    kern<<<(unsigned)norm_blocks(p.B, 1, per_sm, smem, sms, 16), THREADS, smem, st>>>(p, ld, nb);
+    const size_t smem = (size_t)g.nb * g.per_slot * p.map.banks * g.ld + 2 * p.map.W * sizeof(float);
+    kern<<<(unsigned)norm_blocks(g.nslots, 1, per_sm, smem, sms, 16), THREADS, smem, st>>>(p, g);
     return cudaGetLastError();
 }
 template <typename T>
-static cudaError_t launch_sample_fwd_t(const NormParams& p, uint32_t ld, int nb, int sms, cudaStream_t st) {
+static cudaError_t launch_sample_fwd_t(const NormParams& p, const SampleGeo& g, int sms, cudaStream_t st) {
     constexpr int V = sizeof(T) == 2 ? 8 : 4;
-#define TM_ARGS (p, ld, nb, sms, st)
+#define TM_ARGS (p, g, sms, st)
     TM_NORM_WARP_ROWS(launch_sample_fwd, T, V, p.map.W)
 #undef TM_ARGS
     return cudaErrorInvalidValue;
 }
 
-static size_t sample_bwd_smem(int H, int W, uint32_t ld) {
-    return (size_t)3 * H * ld + W * sizeof(float) + H * (sizeof(float4) + 3 * sizeof(float2));
-}
-template <typename T, int VA, int NVA, int PARTS, bool CK, int NW>
-static cudaError_t launch_sample_bwd(const NormParams& p, uint32_t ld, uint32_t ldc, int sms, int* nblk,
-                                     cudaStream_t st) {
+template <typename T, int NV, bool CK, int NW>
+static cudaError_t launch_sample_bwd(const NormParams& p, const SampleGeo& g, int sms, int* nblk, cudaStream_t st) {
     constexpr int THREADS = NW * 32;
-    auto kern = ln_sample_bwd_kernel<T, VA, NVA, PARTS, CK, NW>;
+    auto kern = ln_sample_bwd_kernel<T, NV, CK, NW>;
     static std::atomic<int> cache[64];
     int per_sm = 0;
     cudaError_t e = norm_resident(kern, THREADS, kSampleSmem, cache, &per_sm);
     if (e != cudaSuccess) return e;
-    const size_t smem = sample_bwd_smem(p.map.banks, p.map.W, ld);
-    const long long grid = norm_blocks(p.B, 1, per_sm, smem, sms, kNormBlocksPerSm);
+    const size_t smem = sample_bwd_smem(g.per_slot * p.map.banks, p.map.W, g.ld);
+    const long long grid = norm_blocks(g.nslots, 1, per_sm, smem, sms, kNormBlocksPerSm);
     *nblk = (int)grid;
-    kern<<<(unsigned)grid, THREADS, smem, st>>>(p, ld, ldc);
+    kern<<<(unsigned)grid, THREADS, smem, st>>>(p, g);
     return cudaGetLastError();
 }
 template <typename T, bool CK>
-static cudaError_t launch_sample_bwd_t(const NormParams& p, uint32_t ld, uint32_t ldc, int sms, int* nblk,
-                                       cudaStream_t st) {
+static cudaError_t launch_sample_bwd_t(const NormParams& p, const SampleGeo& g, int sms, int* nblk, cudaStream_t st) {
     const int W = p.map.W;
-#define X(VA, NVA, PARTS, NW) \
-    if (W <= 32 * VA * NVA * PARTS) return launch_sample_bwd<T, VA, NVA, PARTS, CK, NW>(p, ld, ldc, sms, nblk, st);
-    if constexpr (sizeof(T) == 2) { X(8, 1, 1, 8) X(8, 2, 1, 8) X(8, 3, 1, 16) X(8, 4, 1, 16) }
-    else { X(4, 1, 1, 8) X(4, 2, 1, 8) X(4, 4, 1, 16) X(4, 8, 1, 16) }
+    constexpr int V = sizeof(T) == 2 ? 8 : 4;
+#define X(NV, NW) \
+    if (W <= 32 * V * NV) return launch_sample_bwd<T, NV, CK, NW>(p, g, sms, nblk, st);
+    X(1, 8) X(2, 8)
+    if constexpr (V == 8) { X(3, 16) }
+    X(4, 16)
+    if constexpr (V == 4) { X(8, 16) }
 #undef X
     return cudaErrorInvalidValue;
 }
@@ -1108,10 +1159,10 @@ cudaError_t launch_ln_fwd(int dtype, const NormParams& p, int sms, cudaStream_t 
     const int esz = dtype == 1 ? 2 : 4;
     if (p.map.layout == 1 && p.res == p.x && p.map.T == p.map.banks && p.map.W <= 1024 &&
         (size_t)p.map.banks * p.map.W * esz >= kSampleLeast) {
-        const uint32_t ld = sample_ld(p.map.W * esz, p.map.dh * esz);
-        const int nb = sample_slots((size_t)p.map.banks * ld, 2 * p.map.W * sizeof(float));
-        if (nb) return dtype == 1 ? launch_sample_fwd_t<__nv_bfloat16>(p, ld, nb, sms, st)
-                                  : launch_sample_fwd_t<float>(p, ld, nb, sms, st);
+        SampleGeo g = sample_geo(p.B, p.map.banks, p.map.W, p.map.dh, esz, sms);
+        g.nb = sample_slots((size_t)g.per_slot * p.map.banks * g.ld, 2 * p.map.W * sizeof(float));
+        if (g.nb) return dtype == 1 ? launch_sample_fwd_t<__nv_bfloat16>(p, g, sms, st)
+                                    : launch_sample_fwd_t<float>(p, g, sms, st);
     }
     const bool vec = norm_vec(dtype, p.map.W);
     return dtype == 1 ? launch_ln_fwd_t<__nv_bfloat16>(p, vec, sms, st) : launch_ln_fwd_t<float>(p, vec, sms, st);
@@ -1134,14 +1185,14 @@ cudaError_t launch_ln_bwd(int dtype, const NormParams& p, bool self, void* dgain
         ProfileScope ps_("layer_norm_bwd", st);
         const int esz = dtype == 1 ? 2 : 4;
         const bool vec = norm_vec(dtype, p.map.W);
-        const uint32_t ld = sample_ld(p.map.W * esz, p.map.dh * esz), ldc = sample_ld(p.map.W, p.map.dh);
-        const bool sample = self && (size_t)p.map.banks * p.map.W * esz >= kSampleLeast &&
-                            (!ck || (p.map.W % 16 == 0 && ldc <= ld)) &&
-                            sample_bwd_smem(p.map.banks, p.map.W, ld) <= kSampleSmem;
+        const SampleGeo g = sample_geo(p.B, p.map.banks, p.map.W, p.map.dh, esz, sms);
+        const bool sample = self && p.map.banks <= 256 &&
+                            (!ck || (p.map.W % 16 == 0 && g.ldc <= g.ld)) &&
+                            sample_bwd_smem(g.per_slot * p.map.banks, p.map.W, g.ld) <= kSampleSmem;
 #define X(FN, ...)                                                                                            \
     e = dtype == 1 ? (ck ? FN<__nv_bfloat16, true>(__VA_ARGS__) : FN<__nv_bfloat16, false>(__VA_ARGS__))      \
                    : (ck ? FN<float, true>(__VA_ARGS__) : FN<float, false>(__VA_ARGS__))
-        if (sample) X(launch_sample_bwd_t, p, ld, ldc, sms, &nblk, st);
+        if (sample) X(launch_sample_bwd_t, p, g, sms, &nblk, st);
         else if (self) X(launch_ln_self_t, p, sms, &nblk, st);
         else X(launch_ln_bwd_t, p, vec, sms, &nblk, st);
 #undef X
