@@ -65,6 +65,10 @@ __device__ __forceinline__ float2 act_slope2(float2 z) {
 // dy, z, dz are [B, cols] with cols = banks * N; a thread owns V columns and walks down its block's
 // rows; the sums over a block's rows go to part [gridDim.y][cols] (in a fixed order).  SRC: what z is
 // read from.  dz may be NULL (no activation: dz is dy, only the sums are wanted).
+// One pass, bound by memory: 8192 x 48 x 1536 bf16 with z whole 562 us (6.4 TB/s); from the checkpoint 513
+// to 600 (a sixth fewer bytes, but the codes' conversion and the slope then take as long as the bus).
+// dz is rounded to bf16, the operand type of both contractions that read it: its half step, 2^-8, is of the
+// size of the one in y and dominates the error of dx and dw.
 enum ZSrc : int { Z_NONE = 0, Z_FULL = 1, Z_CK8 = 2 };
 constexpr int kActX = 64, kActY = 4;
 
@@ -165,7 +169,8 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict_
 }
 
 // The same for many parts of few columns (the bias gradient's): a block takes 32 columns, eight slices of the
-// parts side by side, then the slices in order.
+// parts side by side, then the slices in order.  64 parts of 12288 columns: 9 us, 12 with a thread a column;
+// for up to 8 parts (a split contraction's, of many columns) the slices would be a part each.
 template <typename T>
 __global__ void __launch_bounds__(256) sum_parts_tall_kernel(const float* __restrict__ part, int R, long long n,
                                                              T* __restrict__ out) {
@@ -188,7 +193,9 @@ __global__ void __launch_bounds__(256) sum_parts_tall_kernel(const float* __rest
 
 // ------------------------------------------------------------------ fp32 contractions
 // D[g][m][n] = sum_k A[g][m][k] B[g][n][k] with every stride given, 64 x 64 tiles, slabs of 16, 4 x 4
-// outputs a thread; the forward's epilogue as in tm_linear.cuh.
+// outputs a thread; the forward's epilogue as in tm_linear.cuh.  The path of the small fp32 stack: exact
+// products in fp32, no tensor cores.  256 x 16 banks x 256 -> 256 27 us, 4096 x 16 x 512 -> 512 28 TFLOP/s,
+// about a third of the CUDA cores' rate: bound by the shared-memory reads of a 4 x 4 tile.
 struct SimtLin {
     const float *a, *b, *bias, *add;
     float *d, *z;

@@ -10,16 +10,22 @@
 // Tile: 128 rows x BN columns, contraction in slabs of 64, 128-byte swizzle; edges in any direction are
 // zeros from the tensor maps (loads past an extent) and predicates (stores), so sizes need only be
 // multiples of 8 (16-byte strides).  Persistent CTAs, one per SM: warp 0 issues the TMA loads, warp 1
-// the MMAs, warps 2-9 are the epilogue (two per TMEM lane quarter, each half of the columns).  Two
+// the MMAs, the others (16 for 256 columns, 8 for 128) are the epilogue, 32 rows x 64 columns each.  Two
 // accumulators in TMEM let the epilogue of a tile overlap the MMAs of the next.
 //
 // Pair mode (PAIR): a cluster of two CTAs on 256 rows, each holding its 128 A rows and half of the B
 // rows, one tcgen05.mma.cta_group::2 for both.  A tile's operands are then 32 KB a slab and SM instead
-// of 48: the plain form is bound by what the L2 delivers to the SMs.
+// of the 48 of a single CTA's 128 x 256, which was bound by what the L2 delivers to the SMs (87 us against
+// 73 for 8 banks of 4096 x 768 -> 1536).  Shapes with few rows, columns or tiles take 128 x 128 tiles.
 //
-// Epilogue: 32 columns at a time, the next 32 on their way from TMEM.  Eight warps share the activation:
-// per 128 x 256 tile it costs one exponential per element (2048 cycles of the SM's 16 per cycle), which
-// a contraction of depth 256 (2048 tensor cycles) covers.
+// Epilogue: 32 columns at a time from TMEM, the box out by a bulk store.  Per 128 x 256 tile the activation
+// costs one exponential per element (2048 cycles of the SM's 16 per cycle), which a contraction of depth 256
+// (2048 tensor cycles) just covers; 8 epilogue warps did not keep up with it, 16 do.
+//
+// Measured (gelu): 48 banks of 8192 x 768 -> 1536 795 us, 1168 TFLOP/s (0.70 of the cuBLAS rate measured on
+// this kind of GPU for one square bf16 product, 0.84 of its rate under the power cap; dX 1347, dW 1373
+// TFLOP/s); with z kept 920, with its checkpoint 943.  8 banks of 4096 x 768 -> 1536 74 us, 16 of 4096 x 256 ->
+// 1024 57 us, where 27 would move the bytes: a tile is 4 slabs, and its 16 warps' epilogue as long as its loads.
 #pragma once
 #include "tm_ckpt8.cuh"
 #include "tm_gemm.cuh"

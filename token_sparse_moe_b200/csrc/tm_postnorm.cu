@@ -133,9 +133,12 @@ bool map_mats_f32(CUtensorMap* m, const void* base, uint64_t mats, int R, int W)
 
 // Tile shape and contraction splits of one contraction.  Estimated time in units of one 64-deep slab of
 // a pair's 256 x 256 tile (about 512 tensor-core cycles): full waves of tiles times slabs, plus a tile's
-// fill and epilogue.  A 128 x 128 tile does a quarter of the work on half the SMs and is bound by its
-// loads (as many bytes per SM as the pair's); a split adds the partial sums' way out and back through
-// memory and one more launch.
+// fill and epilogue.  A 128 x 128 tile does a quarter of the work on half the SMs: its slab takes 0.6 of a
+// pair's, bound by its loads (as many bytes per SM), or 0.95 where both operands come in 64-row boxes (dW);
+// a split adds the partial sums' way out and back through memory and one more launch.  Measured, pair / tile:
+// forward 16 banks of 4096 x 256 -> 1024 45 / 53 us, 8 of 4096 x 768 -> 1536 71 / 90, 4 of 1000 x 512 -> 512
+// 11.2 / 8.3, 16 of 333 x 384 -> 264 11.2 / 8.2; dW of 8 x 3829 x 168 x 600 as 1 / 2 / 3 / 4 runs 40 / 26 / 21 / 28,
+// of 48 x 1419 x 888 x 568 99 / 156 / 187 / 215.  Over 60 random dW the choice is 1.7 % above the best of all.
 struct LinPlan {
     bool pair;
     int splits, split_slabs;
@@ -146,7 +149,7 @@ LinPlan plan_contraction(long long groups, int rows, int cols, int depth, bool m
     double best_cost = 1e300;
     for (int pair = 1; pair >= 0; --pair) {
         const int bm = pair ? 256 : 128;
-        const double unit = pair ? 1.0 : 0.6;
+        const double unit = pair ? 1.0 : may_split ? 0.95 : 0.6;
         const int units = pair ? sms / 2 : sms;
         if (pair && (rows <= 128 || cols <= 128 || units < 1)) continue;
         const long long tiles = groups * ((rows + bm - 1) / bm) * ((cols + bm - 1) / bm);
