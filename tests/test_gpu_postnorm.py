@@ -154,6 +154,9 @@ def test_layer_norm_of_many_small_samples(dtype, B, T, D, H, ckpt):
 # ------------------------------------------------------------------ per-token linear layer
 LINEAR = [(1, 1, 8, 8), (1, 3, 64, 128), (5, 2, 72, 40), (64, 2, 64, 64), (128, 1, 256, 256), (129, 2, 128, 264),
           (200, 3, 136, 328), (300, 2, 320, 96), (33, 1, 768, 1536), (1000, 1, 40, 72), (700, 2, 384, 520)]
+# (enough rows, columns and banks for the tiles of two SMs, with edges in every direction: the forward, dX, dW
+# whole and dW split, in turn)
+LINEAR_LARGE = [(390, 30, 264, 200), (450, 24, 200, 392), (4000, 2, 264, 392)]
 LINEAR_F32 = [(1, 1, 1, 1), (3, 2, 5, 7), (65, 2, 33, 70), (64, 8, 64, 128), (17, 1, 81, 196)]
 
 
@@ -201,6 +204,13 @@ def linear_case(dtype, B, banks, K, N, act, bias_, res_, save):
                                                  ("silu", True, True, "full"), ("relu", False, True, "ckpt8")])
 @pytest.mark.parametrize("B,banks,K,N", LINEAR)
 def test_linear_bf16(B, banks, K, N, act, bias_, res_, save):
+    linear_case("bf16", B, banks, K, N, act, bias_, res_, save)
+
+
+@pytest.mark.parametrize("act,bias_,res_,save", [("none", True, True, "full"), ("relu", True, False, "ckpt8"),
+                                                 ("gelu", True, True, "full"), ("silu", False, True, "ckpt8")])
+@pytest.mark.parametrize("B,banks,K,N", LINEAR_LARGE)
+def test_linear_bf16_on_pairs(B, banks, K, N, act, bias_, res_, save):
     linear_case("bf16", B, banks, K, N, act, bias_, res_, save)
 
 

@@ -355,9 +355,9 @@ __device__ __forceinline__ void zero_sums(float2 (&dg)[NV][Pairs<V>::N], float2 
         for (int k = 0; k < Pairs<V>::N; ++k) dg[i][k] = db[i][k] = make_float2(0.f, 0.f);
 }
 
-// The block's sums of dgain and dbias over its row groups (group grp's thread gl holds columns c0 + (gl + G i) V
-// .. below c1), in a fixed order: through shared memory, one of the two at a time and `room` groups at a
-// time; sm holds room * W floats and is free when this is called.
+// The block's sums of dgain and dbias over its row groups (group grp's thread gl holds columns (gl + G i) V ..),
+// in a fixed order: through shared memory, one of the two at a time and `room` groups at a time; sm holds
+// room * W floats and is free when this is called.
 template <int V, int NV, int G>
 __device__ __forceinline__ void ln_store_partials(const NormParams& p, float* sm, int room, int groups, int grp, int gl,
                                                   const float2 (&dg)[NV][Pairs<V>::N],
