@@ -157,6 +157,8 @@ LINEAR = [(1, 1, 8, 8), (1, 3, 64, 128), (5, 2, 72, 40), (64, 2, 64, 64), (128, 
 # (enough rows, columns and banks for the tiles of two SMs, with edges in every direction: the forward, dX, dW
 # whole and dW split, in turn)
 LINEAR_LARGE = [(390, 30, 264, 200), (450, 24, 200, 392), (4000, 2, 264, 392)]
+# (one sample: contractions of more than one trip, columns that end inside a block of 32)
+LINEAR_ONE = [(1, 5, 1032, 40), (1, 2, 520, 264), (1, 40, 768, 136), (1, 1, 16, 8)]
 LINEAR_F32 = [(1, 1, 1, 1), (3, 2, 5, 7), (65, 2, 33, 70), (64, 8, 64, 128), (17, 1, 81, 196)]
 
 
@@ -204,6 +206,15 @@ def linear_case(dtype, B, banks, K, N, act, bias_, res_, save):
                                                  ("silu", True, True, "full"), ("relu", False, True, "ckpt8")])
 @pytest.mark.parametrize("B,banks,K,N", LINEAR)
 def test_linear_bf16(B, banks, K, N, act, bias_, res_, save):
+    linear_case("bf16", B, banks, K, N, act, bias_, res_, save)
+
+
+@pytest.mark.parametrize("act,bias_,res_,save", [("none", True, True, "full"), ("none", False, False, "full"),
+                                                 ("relu", True, False, "full"), ("gelu", True, True, "ckpt8"),
+                                                 ("gelu", False, False, "full"), ("silu", True, True, "ckpt8"),
+                                                 ("silu", False, True, "full"), ("relu", False, True, "ckpt8")])
+@pytest.mark.parametrize("B,banks,K,N", LINEAR_ONE)
+def test_linear_bf16_of_one_sample(B, banks, K, N, act, bias_, res_, save):
     linear_case("bf16", B, banks, K, N, act, bias_, res_, save)
 
 

@@ -148,6 +148,8 @@ cudaError_t launch_ln_fwd(int dtype, const NormParams& p, int sms, cudaStream_t 
 cudaError_t launch_ln_bwd(int dtype, const NormParams& p, bool self, void* dgain, void* dbias, int sms,
                           cudaStream_t st);
 cudaError_t launch_linear_simt(const SimtLin& p, cudaStream_t st);
+struct RowLin;
+cudaError_t launch_linear_row(int banks, int act, int save, const RowLin& p, cudaStream_t st);
 // Tensor maps of one contraction: operands, D (or fp32 partial sums), addend (any valid map where there is
 // none)
 struct LinMaps {

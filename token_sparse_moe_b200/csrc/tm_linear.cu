@@ -1,5 +1,5 @@
-// tm_linear.cu -- the per-token linear layer beside its tensor-core contractions (tm_linear.cuh): the
-// activation's derivative with the bias gradient's column sums, the sums of partial results, the fp32
+// tm_linear.cu -- the per-token linear layer beside its tensor-core contractions (tm_linear.cuh): the forward
+// of one sample, the activation's derivative with the bias gradient's column sums, the sums of partial results, the fp32
 // form of the contractions on CUDA cores, and the launchers.
 #include <string.h>
 
@@ -268,6 +268,101 @@ __global__ void __launch_bounds__(256) linear_simt_kernel(const SimtLin p) {
             p.d[o + j] = y;
         }
     }
+}
+
+// ------------------------------------------------------------------ one sample
+// The bf16 forward of a single sample, where the weights' one pass through memory is all there is.  A block
+// owns 32 columns of a bank (one block of the checkpoint's codes), a warp four of them, its lanes along the
+// contraction in vectors of 8, eight vectors of weights in flight a lane; sums in fp32, joined by shuffles in
+// a fixed order; then the first warp has a column a lane.  No tile, barrier or x from shared memory: 48 banks of
+// 768 -> 1536 take 20.7 us (5.5 TB/s of weights; the tensor-core tiles 24.1), 40 of 1024 -> 2048 28.5 (37.7), 1 of
+// 1024 -> 2048 4.1 (9.0).  From two samples on, their x and sums crowd out the loads (33 us to the tiles' 22).
+struct RowLin {
+    const __nv_bfloat16 *x, *w, *bias, *res;
+    __nv_bfloat16 *y, *z;
+    int8_t *codes, *exps;
+    int K, N, nblk;
+};
+
+template <int ACT, int SAVE>
+__global__ void __launch_bounds__(256, 4) linear_row_kernel(const RowLin p) {
+    __shared__ float sums[32];
+    constexpr int U = 2;
+    const int bank = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n0 = blockIdx.x * 32, kv = p.K / 8;
+    const size_t o = (size_t)bank * p.N + n0 + lane;
+    const bool in = warp == 0 && n0 + lane < p.N;
+    float bias = 0.f, res = 0.f;
+    if (in && p.bias) bias = to_f(__ldg(p.bias + o));
+    if (in && p.res) res = to_f(__ldg(p.res + o));
+    float sum = 0.f;                                       // of column 4 warp + (lane >> 3) in every lane
+    if (n0 + 4 * warp < p.N) {                             // N is a multiple of 8: whole fours
+        const __nv_bfloat16* w = p.w + ((size_t)bank * p.N + n0 + 4 * warp) * p.K;
+        const __nv_bfloat16* x = p.x + (size_t)bank * p.K;
+        float2 acc[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = make_float2(0.f, 0.f);
+        for (int c0 = lane; c0 < kv; c0 += 32 * U) {
+            Pack<__nv_bfloat16, 8> wv[U][4], xw[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c0 + 32 * u < kv) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) wv[u][j].load(w + (size_t)j * p.K + (c0 + 32 * u) * 8);
+                    xw[u].load(x + (c0 + 32 * u) * 8);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c0 + 32 * u < kv) {
+                    float2 xv[4];
+                    xw[u].get(xv);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float2 v[4];
+                        wv[u][j].get(v);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) acc[j] = fma2(v[k], xv[k], acc[j]);
+                    }
+                }
+        }
+        // four sums over the warp: halves exchanged, so that after two steps a lane holds one column's
+        float t[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t[j] = acc[j].x + acc[j].y;
+        const bool h1 = lane & 16, h0 = lane & 8;
+        const float a = (h1 ? t[2] : t[0]) + __shfl_xor_sync(0xffffffffu, h1 ? t[0] : t[2], 16);
+        const float b = (h1 ? t[3] : t[1]) + __shfl_xor_sync(0xffffffffu, h1 ? t[1] : t[3], 16);
+        sum = (h0 ? b : a) + __shfl_xor_sync(0xffffffffu, h0 ? a : b, 8);
+#pragma unroll
+        for (int k = 4; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    }
+    if ((lane & 7) == 0) sums[4 * warp + (lane >> 3)] = sum;
+    __syncthreads();
+    if (warp != 0) return;
+    float v = in ? sums[lane] + bias : 0.f;
+    if constexpr (SAVE == LIN_KEEP_CK8) {
+        const float2 one[1] = {make_float2(v, 0.f)};
+        uint32_t q[1];
+        const int e = ck8_quantize<1, 32>(one, q);
+        if (in) p.codes[o] = (int8_t)q[0];
+        if (lane == 0) p.exps[bank * p.nblk + blockIdx.x] = (int8_t)e;
+    }
+    if (!in) return;
+    if constexpr (SAVE == LIN_KEEP_FULL) p.z[o] = __float2bfloat16(v);
+    p.y[o] = __float2bfloat16(lin_act2<ACT>(make_float2(v, 0.f)).x + res);
+}
+
+cudaError_t launch_linear_row(int banks, int act, int save, const RowLin& p, cudaStream_t st) {
+    ProfileScope ps_("linear_row", st);
+    const dim3 grid((p.N + 31) / 32, banks);
+#define X(ACT_, SAVE_) \
+    if (act == ACT_ && (act == LIN_NONE || save == SAVE_)) linear_row_kernel<ACT_, SAVE_><<<grid, 256, 0, st>>>(p);
+    X(LIN_NONE, LIN_KEEP_NOTHING)
+    X(LIN_RELU, LIN_KEEP_NOTHING) X(LIN_RELU, LIN_KEEP_FULL) X(LIN_RELU, LIN_KEEP_CK8)
+    X(LIN_GELU, LIN_KEEP_NOTHING) X(LIN_GELU, LIN_KEEP_FULL) X(LIN_GELU, LIN_KEEP_CK8)
+    X(LIN_SILU, LIN_KEEP_NOTHING) X(LIN_SILU, LIN_KEEP_FULL) X(LIN_SILU, LIN_KEEP_CK8)
+#undef X
+    return cudaGetLastError();
 }
 
 // ------------------------------------------------------------------ launchers

@@ -359,6 +359,14 @@ tm_status tm_pertoken_linear(const void* x, const void* residual, const tm_shape
         p.act = w->act;
         return cuda_status(launch_linear_simt(p, st));
     }
+    const int save = z_opt ? LIN_KEEP_FULL : save_opt ? LIN_KEEP_CK8 : LIN_KEEP_NOTHING;
+    if (g.B == 1 && g.banks <= 65535) {          // the weights' stream alone; the grid has a bank in y
+        const RowLin p{(const __nv_bfloat16*)x, (const __nv_bfloat16*)w->w, (const __nv_bfloat16*)w->bias,
+                       (const __nv_bfloat16*)residual, (__nv_bfloat16*)y, (__nv_bfloat16*)z_opt,
+                       save_opt ? save_opt->codes : nullptr, save_opt ? save_opt->exps : nullptr,
+                       g.K, g.N, (g.N + kCk8Block - 1) / kCk8Block};
+        return cuda_status(launch_linear_row(g.banks, w->act, save, p, st));
+    }
     const LinPlan pl = plan_contraction(g.banks, g.B, g.N, g.K, false, num_sms());
     LinParams p = lin_params(g.banks, g.B, g.N, g.K, pl);
     p.bias = (const __nv_bfloat16*)w->bias;
@@ -374,7 +382,6 @@ tm_status tm_pertoken_linear(const void* x, const void* residual, const tm_shape
         return TM_ERR_CUDA;
     m.r = m.o;
     if (residual && !map_rows(&m.r, residual, g.B, g.banks, g.N, 64, 32)) return TM_ERR_CUDA;
-    const int save = z_opt ? LIN_KEEP_FULL : save_opt ? LIN_KEEP_CK8 : LIN_KEEP_NOTHING;
     return cuda_status(launch_linear_fwd(pl.pair, w->act, save, m, p, num_sms(), st));
 }
 
