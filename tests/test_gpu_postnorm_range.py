@@ -1,0 +1,56 @@
+"""GPU tests of the per-token linear layer's slopes over every finite pre-activation of bf16 (each of the 65280
+values, in bf16 and as fp32), through identity weights, against the float64 oracle.
+
+The bounds, derived before any run; h is half a step of the storage type relative to the value:
+
+* slopes: the documented absolute bound, and h of the value.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import postnorm as P
+from postnorm_util import DEV, DT, HALF, U, check, f64
+from token_sparse_moe_b200 import api
+
+pytestmark = pytest.mark.gpu
+
+
+def every_value(order):
+    """All finite bf16 values as [8160, 8]: by their bits, or shuffled so that neighbours differ wildly."""
+    bits = np.arange(65536, dtype=np.uint32)
+    bits = bits[(bits & 0x7F80) != 0x7F80]
+    if order == "shuffled":
+        bits = np.random.default_rng(5).permutation(bits)
+    return (bits << 16).view(np.float32).reshape(-1, 8)
+
+
+def eye(banks, dtype):
+    return torch.eye(8, dtype=DT[dtype], device=DEV).expand(banks, 8, 8).contiguous()
+
+
+def every_slope(act, dtype, save, order):
+    """(pre-activations that the backward works from, dz for dy = 1) of all finite values."""
+    z = torch.from_numpy(every_value(order)).reshape(8160, 1, 8).to(DT[dtype]).to(DEV)
+    saved = z if save == "full" else api.checkpoint8_pack(z)
+    if save == "ckpt8":
+        z = api.checkpoint8_unpack(saved)
+    one = torch.ones_like(z)
+    dx, g = api.pertoken_linear_backward(one, one, api.Linear(eye(1, dtype), torch.zeros(1, 8, dtype=DT[dtype], device=DEV), act),
+                                         saved)
+    assert torch.isfinite(g["dw"]).all() and torch.isfinite(g["db"]).all()
+    return f64(z), dx                     # dx = dz through the identity
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("save,order", [("full", "by bits"), ("full", "shuffled"), ("ckpt8", "by bits")])
+@pytest.mark.parametrize("act", ["relu", "gelu", "silu"])
+def test_slope_of_every_finite_value(dtype, save, order, act):
+    """Slopes of bf16 to the documented absolute bound (gelu 2e-5, silu 1e-5 with its roundings; fp32 16 u of 1 + |z| up
+    to 20, past which the slope is 0 or 1 to 1e-7)."""
+    z, dz = every_slope(act, dtype, save, order)
+    want = P.act_slope(z, act)
+    t = 0.0 * z
+    if act != "relu":
+        t = t + (16 * U * (1 + np.minimum(np.abs(z), 20)) if dtype == "f32" else {"gelu": 2e-5, "silu": 1e-5}[act])
+    check(act, dz, want, t + HALF[dtype] * (np.abs(want) + t))

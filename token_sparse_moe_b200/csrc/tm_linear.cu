@@ -40,8 +40,10 @@ __device__ __forceinline__ float2 act_slope2(float2 z) {
     if constexpr (ACT == LIN_GELU) {
         // gelu'(-a) = Q(a) - a phi(a) = 1 - gelu'(a) = exp(-a^2 / 2) U(a), a >= 0, with U(a) = Q(a) / exp(-a^2 / 2)
         // - a / sqrt(2 pi) as a polynomial of degree 6 (weighted least squares towards the smallest maximum on
-        // [0, 5]): 1.6e-5 off at most, a hundredth of bf16's half step of the slopes it is multiplied into
-        const float2 a = make_float2(fabsf(z.x), fabsf(z.y));
+        // [0, 5]): 1.6e-5 off at most, a hundredth of bf16's half step of the slopes it is multiplied into.  a is
+        // held at 16, where the exponential (of z itself, so that NaN stays) is 0 already: past 8.9e6 the
+        // polynomial would be infinite, and its product with 0 NaN
+        const float2 a = make_float2(fminf(fabsf(z.x), 16.f), fminf(fabsf(z.y), 16.f));
         const float2 x = mul2(mul2(z, z), f2(-0.72134752044448170f));       // -a^2 / 2 in powers of two
         float2 u = f2(7.04223057e-4f);
         u = fma2(u, a, f2(-8.04183446e-3f));
