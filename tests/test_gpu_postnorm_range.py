@@ -3,7 +3,13 @@ values, in bf16 and as fp32), through identity weights, against the float64 orac
 
 The bounds, derived before any run; h is half a step of the storage type relative to the value:
 
-* slopes: the documented absolute bound, and h of the value.
+* slopes: the documented absolute bound, and h of the value;
+* gelu's slope from -1.5 down keeps its relative precision as far as its exponential is a normal fp32 number: the
+  documented 1.5e-4 in bf16, an exponent of up to 126 with three roundings (3 * 126 u ln 2 = 1.6e-5), and the exponential,
+  the reciprocal and five steps whose cancellation at most doubles them (16 u): 2e-4.  In fp32 the exponent's rounding
+  is multiplied by at most a^2 / 2 <= 90, erfcf's by a^2 <= 180 of a term that is a third of the other at 1.5 and less
+  beyond, and expf and erfcf are good to a few u: below 2 * 300 u < 1e-4.  Below the normal numbers the slope may be
+  taken as 0: at most 6 * 2^-126 there.
 """
 import numpy as np
 import pytest
@@ -54,3 +60,12 @@ def test_slope_of_every_finite_value(dtype, save, order, act):
     if act != "relu":
         t = t + (16 * U * (1 + np.minimum(np.abs(z), 20)) if dtype == "f32" else {"gelu": 2e-5, "silu": 1e-5}[act])
     check(act, dz, want, t + HALF[dtype] * (np.abs(want) + t))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("save", ["full", "ckpt8"])
+def test_slope_of_gelu_keeps_its_precision_in_the_tail(dtype, save):
+    z, dz = every_slope("gelu", dtype, save, "by bits")
+    want = P.act_slope(z, "gelu")
+    t = np.where(z <= -1.5, {"bf16": 2e-4, "f32": 1e-4}[dtype], np.inf) * np.abs(want) + 2.0 ** -123
+    check("gelu", dz, want, t + HALF[dtype] * (np.abs(want) + t))
