@@ -1,8 +1,14 @@
-"""GPU tests of the per-token linear layer's slopes over every finite pre-activation of bf16 (each of the 65280
+"""GPU tests of the per-token linear layer's activations and slopes over every finite pre-activation of bf16 (each of the 65280
 values, in bf16 and as fp32), through identity weights, against the float64 oracle.
 
 The bounds, derived before any run; h is half a step of the storage type relative to the value:
 
+* bf16 silu, z < 0: its exponential is e^-|z|, whose exponent of up to 126 in fp32 with two roundings is off by
+  2 * 126 * 2^-24 = 1.5e-5; the exponential, the reciprocal and five steps (2^-20): 2e-4 of the value, as far as the
+  exponential is a normal fp32 number (2^-126).  Below that it is taken as 0: silu is at most 90 * 2^-126 < 2^-119 there.
+* z >= 0: the value is z less a tail with the same bound, and 4 u of z.
+* fp32: expf is good to a few u, its argument's rounding is multiplied by at most |z| <= 90 before the tail leaves
+  the normal numbers: 4 * 90 * u < 3e-5.
 * slopes: the documented absolute bound, and h of the value;
 * gelu's slope from -1.5 down keeps its relative precision as far as its exponential is a normal fp32 number: the
   documented 1.5e-4 in bf16, an exponent of up to 126 with three roundings (3 * 126 u ln 2 = 1.6e-5), and the exponential,
@@ -20,6 +26,7 @@ from postnorm_util import DEV, DT, HALF, U, check, f64
 from token_sparse_moe_b200 import api
 
 pytestmark = pytest.mark.gpu
+GONE = 2.0 ** -119                        # what an exponential below the normal fp32 numbers may have held
 
 
 def every_value(order):
@@ -33,6 +40,28 @@ def every_value(order):
 
 def eye(banks, dtype):
     return torch.eye(8, dtype=DT[dtype], device=DEV).expand(banks, 8, 8).contiguous()
+
+
+def forward_bound(z, y, act, dtype):
+    rel = {"f32": 3e-5, "bf16": {"silu": 2e-4}.get(act, 0.0)}[dtype]
+    tail = y if act == "relu" else np.where(z < 0, y, y - z)          # of positive z: z less the tail
+    t = 0.0 * z if act == "relu" else rel * np.abs(tail) + GONE + 4 * U * np.maximum(z, 0)
+    return t + HALF[dtype] * (np.abs(y) + t)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("form", ["many", "one"])
+@pytest.mark.parametrize("order", ["by bits", "shuffled"])
+@pytest.mark.parametrize("act", ["relu", "silu"])
+def test_activation_of_every_finite_value(dtype, form, order, act):
+    """`many`: 8160 samples of one bank; `one`: one sample of 8160 banks."""
+    z = every_value(order)
+    shape = (8160, 1, 8) if form == "many" else (1, 8160, 8)
+    x = torch.from_numpy(z).reshape(shape).to(DT[dtype]).to(DEV)
+    y = api.pertoken_linear(x, api.Linear(eye(shape[1], dtype), None, act))
+    z = z.astype(np.float64).reshape(shape)
+    want = P.act(z, act)
+    check(act, y, want, forward_bound(z, want, act, dtype))
 
 
 def every_slope(act, dtype, save, order):

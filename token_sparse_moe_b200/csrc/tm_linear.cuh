@@ -125,9 +125,10 @@ __device__ __forceinline__ float2 gauss_tail2(float2 a) {
 }
 
 // Two activations.  gelu(z) = z Phi(z) = max(z, 0) - |z| Q(|z|): both terms keep their relative
-// precision in the negative tail.  silu(z) = z / (1 + e^-z), one reciprocal for two (of the product of
-// the denominators; z is held above -44 inside the exponential, where silu is below 1e-17, so that the
-// product stays finite).  NaN comes out as NaN, +inf as +inf, -inf as 0 (relu, gelu) or -0 or NaN (silu).
+// precision in the negative tail.  silu(z) = z / (1 + e^-z) for z >= 0 and z e^z / (1 + e^z) below, from t = e^-|z|:
+// the denominators are between 1 and 2, so that one reciprocal of the product of two serves both, and a
+// value depends on its neighbour's by a rounding at most (a NaN's exponential is 0 there).  t below 2^-126 is 0: silu is
+// below 2^-119 there.  NaN comes out as NaN, +inf as +inf, -inf as -0 or 0 (relu, gelu) or NaN (silu: inf / inf).
 template <int ACT>
 __device__ __forceinline__ float2 lin_act2(float2 z) {
     if constexpr (ACT == LIN_RELU) return make_float2(max_nan(z.x, 0.f), max_nan(z.y, 0.f));
@@ -138,9 +139,10 @@ __device__ __forceinline__ float2 lin_act2(float2 z) {
     }
     if constexpr (ACT == LIN_SILU) {
         const float kL = -1.4426950408889634f;   // -log2(e)
-        const float d0 = 1.f + ex2_approx(kL * fmaxf(z.x, -44.f)), d1 = 1.f + ex2_approx(kL * fmaxf(z.y, -44.f));
+        const float t0 = ex2_approx(fmaxf(kL * fabsf(z.x), -150.f)), t1 = ex2_approx(fmaxf(kL * fabsf(z.y), -150.f));
+        const float d0 = 1.f + t0, d1 = 1.f + t1;
         const float r = rcp_approx(d0 * d1);
-        return make_float2(z.x * (r * d1), z.y * (r * d0));
+        return make_float2((z.x >= 0.f ? z.x : z.x * t0) * (r * d1), (z.y >= 0.f ? z.y : z.y * t1) * (r * d0));
     }
     return z;
 }
