@@ -1,0 +1,34 @@
+"""GPU tests of the post-norm block's binding: what a caller may hand in, and what is refused before a launch."""
+import numpy as np
+import pytest
+import torch
+
+from postnorm_util import DEV, draw
+from token_sparse_moe_b200 import _abi as A
+from token_sparse_moe_b200 import api
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-6
+
+
+def test_workspace_of_the_caller():
+    """Of any dtype, dense and on the call's device; anything else is refused, whatever its size."""
+    rng = np.random.default_rng(1)
+    x, _ = draw(rng, (70, 3, 96), "bf16")
+    dy, _ = draw(rng, (70, 3, 96), "bf16")
+    w, _ = draw(rng, (3, 96, 96), "bf16")
+    sh = api.shape(70, 3, 96, 1, "bf16", EPS)
+    _, saved = api.layer_norm(x, None, A.TM_LAYOUT_ROWS, sh)
+    lin = api.Linear(w, None, "silu")
+    _, z = api.pertoken_linear(x, lin, save="full")
+    norm = lambda ws: api.layer_norm_backward(dy, saved, A.TM_LAYOUT_ROWS, sh, x=x, workspace=ws)
+    linear = lambda ws: api.pertoken_linear_backward(x, dy, lin, z, workspace=ws)
+    for call in (norm, linear):
+        ref = call(None)
+        for ws in (torch.empty(1 << 22, dtype=torch.uint8, device=DEV), torch.empty(1 << 20, dtype=torch.float32, device=DEV),
+                   torch.empty(16, dtype=torch.uint8, device=DEV)):
+            got = call(ws)
+            assert torch.equal(got[0], ref[0]) and all(torch.equal(got[-1][k], ref[-1][k]) for k in ref[-1])
+        for ws in (torch.empty(1 << 22, dtype=torch.uint8), torch.empty(1 << 23, dtype=torch.uint8, device=DEV)[::2]):
+            with pytest.raises(ValueError, match="workspace"):
+                call(ws)

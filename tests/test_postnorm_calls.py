@@ -1,0 +1,23 @@
+"""The post-norm block's binding on the CPU: arguments that are refused before anything is launched."""
+import pytest
+import torch
+
+from token_sparse_moe_b200 import api
+
+
+class _Elsewhere(torch.Tensor):
+    """A dense tensor that says it is on GPU 1."""
+
+    def get_device(self):
+        return 1
+
+
+def test_binding_refuses_a_workspace_that_the_kernels_cannot_use():
+    for ws in (torch.empty(4096, dtype=torch.uint8), torch.empty(4096, dtype=torch.uint8).as_subclass(_Elsewhere)):
+        with pytest.raises(ValueError, match="workspace"):
+            api._scratch(1024, 0, ws)
+    here = torch.empty(2048, dtype=torch.float32).as_subclass(_Elsewhere)
+    with pytest.raises(ValueError, match="workspace"):
+        api._scratch(1024, 1, here[::2])                       # the bytes between its elements are not its own
+    ws, address, nbytes = api._scratch(8192, 1, here)
+    assert ws is here and address == here.data_ptr() and nbytes == 8192

@@ -876,6 +876,20 @@ def _stream_of(stream, dev: int) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _scratch(nbytes: int, dev: int, workspace: Optional[torch.Tensor]):
+    """(tensor, address, bytes) of a workspace of at least nbytes: the caller's, of any dtype, or, where there
+    is none or it is too small, a new one."""
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}, got {tuple(workspace.shape)} "
+                             f"{workspace.dtype} on {workspace.device} with strides {workspace.stride()}")
+        have = workspace.numel() * workspace.element_size()
+        if have >= nbytes:
+            return workspace, workspace.data_ptr(), have
+    workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    return workspace, workspace.data_ptr(), workspace.numel()
+
+
 class _on:
     """Allocates on the stream that the call runs on, so that a workspace given back at the call's
     return is not reused ahead of its kernels by another stream."""
@@ -1045,11 +1059,11 @@ def layer_norm_backward(dy: torch.Tensor, saved: LayerNormSaved, layout: int, sh
     lib_ = A.load()
     w = A.tm_layer_norm_w(banks, width, _arg("gain", gain, (width,), dt, dev), None)
     n = lib_.tm_layer_norm_backward_workspace_bytes(sh, layout, w)
-    ws = _ws(n, dy.device, workspace)
+    ws, pws, nws = _scratch(n, dev, workspace)
     st = lib_.tm_layer_norm_backward(
         px, pres, ck, mean, mean + 4 * B * banks, pdy, layout, sh, w, 1 if residual_is_x else 0, _arg("dx", dx, xshape, dt, dev),
-        None if dres is None else dres.data_ptr(), A.tm_layer_norm_grads(dgain.data_ptr(), dbias.data_ptr()), _p(ws),
-        ws.numel(), _stream_of(None, dev))
+        None if dres is None else dres.data_ptr(), A.tm_layer_norm_grads(dgain.data_ptr(), dbias.data_ptr()), pws,
+        nws, _stream_of(None, dev))
     if st:
         A.check(st, "tm_layer_norm_backward")
     if not mixed and saved.residual:
@@ -1138,11 +1152,11 @@ def pertoken_linear_backward(x: torch.Tensor, dy: torch.Tensor, lin: Linear, sav
         grads["db"] = torch.empty_like(lin.bias)
     lib_ = A.load()
     n = lib_.tm_pertoken_linear_backward_workspace_bytes(sh, c)
-    ws = _ws(n, x.device, workspace)
+    ws, pws, nws = _scratch(n, dev, workspace)
     st = lib_.tm_pertoken_linear_backward(
         _arg("x", x, xshape, dt, dev), _arg("dy", dy, rows, dt, dev), z, ck, _arg("dx_add", dx_add, xshape, dt, dev), sh, c,
         _arg("dx", dx, xshape, dt, dev),
-        A.tm_linear_grads(grads["dw"].data_ptr(), grads["db"].data_ptr() if "db" in grads else None), _p(ws), ws.numel(),
+        A.tm_linear_grads(grads["dw"].data_ptr(), grads["db"].data_ptr() if "db" in grads else None), pws, nws,
         _stream_of(None, dev))
     if st:
         A.check(st, "tm_pertoken_linear_backward")
