@@ -32,3 +32,27 @@ def test_workspace_of_the_caller():
         for ws in (torch.empty(1 << 22, dtype=torch.uint8), torch.empty(1 << 23, dtype=torch.uint8, device=DEV)[::2]):
             with pytest.raises(ValueError, match="workspace"):
                 call(ws)
+
+
+@pytest.mark.parametrize("checkpoint8", [False, True])
+def test_residual_is_x_needs_a_forward_whose_residual_was_x(checkpoint8):
+    """Otherwise dz + Revert(dz) would be handed out where X's gradient is Revert(dz) alone."""
+    rng = np.random.default_rng(2)
+    B, T, D = 5, 8, 64
+    x, _ = draw(rng, (B, T, D), "bf16")
+    other, _ = draw(rng, (B, T, D), "bf16")
+    dy, _ = draw(rng, (B, T, D), "bf16")
+    sh, M = api.shape(B, T, D, T, "bf16", EPS), A.TM_LAYOUT_MIXED
+    for res in (None, other):
+        _, saved = api.layer_norm(x, res, M, sh, checkpoint8=checkpoint8)
+        with pytest.raises((ValueError, A.TMError)):
+            api.layer_norm_backward(dy, saved, M, sh, x=x, residual=res, residual_is_x=True)
+    # X as both: the whole gradient is the sum of the two that come out one by one
+    _, saved = api.layer_norm(x, x, M, sh, checkpoint8=checkpoint8)
+    whole, none, _ = api.layer_norm_backward(dy, saved, M, sh, x=x, residual=x, residual_is_x=True)
+    dx, dres, _ = api.layer_norm_backward(dy, saved, M, sh, x=x, residual=x)
+    assert none is None
+    two = dx.float() + dres.float()
+    off = (whole.float() - two).abs()
+    # the parts are rounded to bf16 each, their sum once more; in fp32 each is good to 100 u of rstd (dn + 1 + n^2) < 30
+    assert (off <= 2.0 ** -8 * (dx.float().abs() + dres.float().abs() + whole.float().abs()) * 1.01 + 4e-4).all()

@@ -966,11 +966,12 @@ def checkpoint8_unpack(ck: Checkpoint8, out: Optional[torch.Tensor] = None, stre
 
 class LayerNormSaved:
     """What layer_norm's backward pass needs: each row's mean and 1 / std (stats [2, B, banks]), and the
-    checkpoint of x + residual unless the caller keeps x and the residual themselves."""
-    __slots__ = ("stats", "ckpt", "residual")
+    checkpoint of x + residual unless the caller keeps x and the residual themselves; whether there was a
+    residual, and whether it was x itself."""
+    __slots__ = ("stats", "ckpt", "residual", "residual_was_x")
 
-    def __init__(self, stats: torch.Tensor, ckpt: Optional[Checkpoint8], residual: bool):
-        self.stats, self.ckpt, self.residual = stats, ckpt, residual
+    def __init__(self, stats: torch.Tensor, ckpt: Optional[Checkpoint8], residual: bool, residual_was_x: bool = False):
+        self.stats, self.ckpt, self.residual, self.residual_was_x = stats, ckpt, residual, residual_was_x
 
     @property
     def mean(self) -> torch.Tensor:
@@ -1006,14 +1007,15 @@ def layer_norm(x: torch.Tensor, residual: Optional[torch.Tensor], layout: int, s
     stats = x.new_empty((2, B, banks), dtype=torch.float32)
     ck = Checkpoint8.like(x, rows) if checkpoint8 else None
     mean = stats.data_ptr()
+    pres = _arg("residual", residual, rows, dt, dev)
     st = A.load().tm_layer_norm(
-        px, _arg("residual", residual, rows, dt, dev), layout, sh,
+        px, pres, layout, sh,
         A.tm_layer_norm_w(banks, width, _arg("gain", gain, (width,), dt, dev), _arg("bias", bias, (width,), dt, dev)),
         _arg("y", y, rows, dt, dev), mean, mean + 4 * B * banks, ck.c("checkpoint", rows, dev) if ck is not None else None,
         _stream_of(None, dev))
     if st:
         A.check(st, "tm_layer_norm")
-    return y, LayerNormSaved(stats, ck, residual is not None)
+    return y, LayerNormSaved(stats, ck, residual is not None, pres == px)
 
 
 def layer_norm_backward(dy: torch.Tensor, saved: LayerNormSaved, layout: int, sh: A.tm_shape,
@@ -1024,7 +1026,7 @@ def layer_norm_backward(dy: torch.Tensor, saved: LayerNormSaved, layout: int, sh
     the forward's, not needed when `saved` holds the checkpoint.  Row layout: the residual's gradient is
     dx itself and returned as such.  Mixed layout: dx is the gradient of the token tensor;
     residual_is_x adds the residual's gradient into it (one tensor X was both) and returns None for
-    dresidual."""
+    dresidual; with a checkpoint, which does not tell the two apart, the forward must have been called so."""
     if stream is not None:
         with _on(stream):
             return layer_norm_backward(dy, saved, layout, sh, gain, x, residual, residual_is_x, dx, workspace)
@@ -1044,6 +1046,9 @@ def layer_norm_backward(dy: torch.Tensor, saved: LayerNormSaved, layout: int, sh
     pdy = _arg("dy", dy, rows, dt, dev)
     px = pres = ck = None
     if saved.ckpt is not None:
+        if residual_is_x and not saved.residual_was_x:
+            raise ValueError("residual_is_x: the forward that kept this checkpoint had "
+                             + ("a residual of its own" if saved.residual else "no residual"))
         ck = saved.ckpt.c("checkpoint", rows, dev)
     else:
         if x is None or (saved.residual and residual is None):
