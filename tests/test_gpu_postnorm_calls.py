@@ -56,3 +56,18 @@ def test_residual_is_x_needs_a_forward_whose_residual_was_x(checkpoint8):
     off = (whole.float() - two).abs()
     # the parts are rounded to bf16 each, their sum once more; in fp32 each is good to 100 u of rstd (dn + 1 + n^2) < 30
     assert (off <= 2.0 ** -8 * (dx.float().abs() + dres.float().abs() + whole.float().abs()) * 1.01 + 4e-4).all()
+
+
+@pytest.mark.parametrize("width", [2 ** 31 - 5, 2 ** 31 - 8])
+def test_checkpoint_of_the_widest_rows(width):
+    """One row of nearly 2^31 values (value by value, and in vectors): codes, exponents and values, piece by piece."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.empty(1, width, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    ck = api.checkpoint8_pack(x)
+    back = api.checkpoint8_unpack(ck)
+    step = 1 << 28
+    for a in range(0, width, step):
+        b = min(width, a + step)
+        want = api.checkpoint8_pack(x[:, a:b].clone())       # (blocks of 32 are the same ones: step is a multiple)
+        assert torch.equal(ck.codes[:, a:b], want.codes) and torch.equal(ck.exps[:, a // 32:(b + 31) // 32], want.exps)
+        assert torch.equal(back[:, a:b], api.checkpoint8_unpack(want))

@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from token_sparse_moe_b200 import _abi as A
 from token_sparse_moe_b200 import api
 
 
@@ -21,3 +22,12 @@ def test_binding_refuses_a_workspace_that_the_kernels_cannot_use():
         api._scratch(1024, 1, here[::2])                       # the bytes between its elements are not its own
     ws, address, nbytes = api._scratch(8192, 1, here)
     assert ws is here and address == here.data_ptr() and nbytes == 8192
+
+
+def test_the_widest_checkpoint_rows_have_their_size():
+    """Of the last widths below 2^31 the blocks are counted right: exponents that would reach into the codes are seen."""
+    lib, x, codes = A.load(), 1 << 40, 1 << 41
+    for width in (2 ** 31 - 1, 2 ** 31 - 31, 2 ** 31 - 32):
+        over = A.tm_ckpt8(codes, codes - 1024)
+        assert lib.tm_checkpoint8_pack(x, A.TM_BF16, 1, width, over, None) == A.TM_ERR_INVALID_ARG
+        assert lib.tm_checkpoint8_unpack(A.tm_ckpt8(codes, x - 1024), A.TM_BF16, 1, width, x, None) == A.TM_ERR_INVALID_ARG

@@ -14,23 +14,24 @@ constexpr int kCk8Threads = 256;
 // The vectors of a thread: unit u of a row holds its values u*V .. u*V + V-1; a row has upr units (its
 // last block filled up to 32 / V of them).  FLAT: rows are whole blocks, so unit u of the whole tensor
 // is its values u*V .. and block u / (32 / V).  Otherwise a thread's units, which are a grid's threads
-// apart, advance row and unit by constants and a carry instead of a division each.
+// apart, advance row and unit by constants and a carry instead of a division each.  (Units are counted without a
+// sign: a row of nearly 2^31 values, filled up to whole blocks, has 2^31 of them.)
 template <typename T, int V, int U, bool PACK, bool FLAT>
 __global__ void __launch_bounds__(kCk8Threads)
     ck8_kernel(T* __restrict__ x, int8_t* __restrict__ codes, int8_t* __restrict__ exps, long long rows, int width,
                int nblk) {
     constexpr int LB = kCk8Block / V;
-    const int upr = nblk * LB;
+    const uint32_t upr = (uint32_t)nblk * LB;
     const long long total = rows * upr;
     const long long nth = (long long)gridDim.x * blockDim.x;
     long long t0 = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     long long row = 0, drow = 0;
-    int s = 0, ds = 0;
+    uint32_t s = 0, ds = 0;
     if (!FLAT) {
         drow = nth / upr;
-        ds = (int)(nth - drow * upr);
+        ds = (uint32_t)(nth - drow * upr);
         row = t0 / upr;
-        s = (int)(t0 - row * upr);
+        s = (uint32_t)(t0 - row * upr);
     }
     // t0 - lane is the warp's first unit: the loop is uniform across the warp (the shuffles need it)
     for (; t0 - (threadIdx.x & 31) < total; t0 += U * nth) {
@@ -44,7 +45,7 @@ __global__ void __launch_bounds__(kCk8Threads)
                 xo[i] = u * V;
                 eo[i] = u / LB;
             } else {
-                in[i] = row < rows && s * V < width;
+                in[i] = row < rows && s * V < (uint32_t)width;
                 xo[i] = row * width + s * V;
                 eo[i] = row * nblk + s / LB;
                 row += drow;
@@ -96,7 +97,7 @@ template <typename T, int V, bool PACK>
 static cudaError_t launch_ck8_one(void* x, void* codes, void* exps, long long rows, int width, int sms,
                                   cudaStream_t st) {
     constexpr int U = 4;
-    const int nblk = (width + kCk8Block - 1) / kCk8Block;
+    const int nblk = ck8_blocks(width);
     const long long total = rows * nblk * (kCk8Block / V);
     const long long all = (total + kCk8Threads - 1) / kCk8Threads, per = (all + U - 1) / U;
     // small inputs: one unit a thread, so that all SMs take part

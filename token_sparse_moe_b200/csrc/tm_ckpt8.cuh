@@ -27,6 +27,8 @@ namespace tml {
 
 constexpr int kCk8Block = 32;
 constexpr int kCk8NaN = 127;      // exponent of a block with a value that is not finite
+// blocks of a row (the sum in 32 bits without a sign: a row may have 2^31 - 1 values)
+__host__ __device__ constexpr int ck8_blocks(int width) { return (int)(((uint32_t)width + kCk8Block - 1) / kCk8Block); }
 
 // Quotients by a fixed divisor d of 0 <= t < 2^31: (umulhi(m, t) + t) >> l, l = ceil(log2 d),
 // m = floor(2^32 (2^l - d) / d) + 1 (division by an invariant integer through multiplication).

@@ -27,7 +27,7 @@ bool spans_ok(const Span (&s)[N]) {
     return true;
 }
 bool ckpt_ok(const tm_ckpt8* c) { return !c || (c->codes && c->exps); }
-size_t ckpt_exps(size_t rows, int width) { return rows * (size_t)((width + kCk8Block - 1) / kCk8Block); }
+size_t ckpt_exps(size_t rows, int width) { return rows * (size_t)ck8_blocks(width); }
 
 // Geometry of normalised rows: as make_geo, but the row layout takes rows of any width.
 tm_status make_norm_geo(const tm_shape* s, int layout, const tm_layer_norm_w* w, Geo* g) {
