@@ -530,7 +530,8 @@ typedef struct { int banks, width, out; tm_act act; const void *w, *bias; } tm_l
  * whole (z_opt [B, banks, out], the storage dtype) or as a checkpoint (save_opt, B * banks rows); both
  * may be NULL, both given is TM_ERR_INVALID_ARG, as is either with TM_ACT_NONE.
  * bf16: width and out multiples of 8 (tensor cores, fp32 accumulation); f32: any sizes (CUDA cores),
- * banks and B / 64 up to 65535.  Others TM_ERR_UNSUPPORTED. */
+ * banks, out / 64 and B / 64 up to 65535; both: banks * width and banks * out up to 2^31 - 256.  Others
+ * TM_ERR_UNSUPPORTED. */
 TM_API tm_status tm_pertoken_linear(const void *x, const void *residual, const tm_shape *shape, const tm_linear_w *w,
                                     void *y, void *z_opt, const tm_ckpt8 *save_opt, void *stream);
 

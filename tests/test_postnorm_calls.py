@@ -31,3 +31,14 @@ def test_the_widest_checkpoint_rows_have_their_size():
         over = A.tm_ckpt8(codes, codes - 1024)
         assert lib.tm_checkpoint8_pack(x, A.TM_BF16, 1, width, over, None) == A.TM_ERR_INVALID_ARG
         assert lib.tm_checkpoint8_unpack(A.tm_ckpt8(codes, x - 1024), A.TM_BF16, 1, width, x, None) == A.TM_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_linear_layers_of_nearly_2_31_columns_are_refused(dtype):
+    """A tile's edge past 2^31 columns is no 32-bit integer."""
+    lib, P = A.load(), lambda i: (i + 1) << 44
+    sh = api.shape(2, 1, 1, 1, dtype)
+    for banks, width, out in ((1, 2 ** 31 - 8, 8), (255, 8421504, 8), (1, 8, 2 ** 31 - 8), (255, 8, 8421504)):
+        w = A.tm_linear_w(banks, width, out, A.TM_ACT_NONE, P(2), None)
+        assert lib.tm_pertoken_linear(P(0), None, sh, w, P(4), None, None, None) == A.TM_ERR_UNSUPPORTED
+        assert lib.tm_pertoken_linear_backward_workspace_bytes(sh, w) == 0

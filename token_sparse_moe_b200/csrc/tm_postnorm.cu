@@ -66,6 +66,7 @@ NormParams norm_params(const Geo& g, const tm_layer_norm_w* w, const void* x, co
 }
 
 // ------------------------------------------------------------------ per-token linear layer
+constexpr long long kLinMostCols = INT32_MAX - 255;   // of all banks together
 struct LinGeo {
     int B, banks, K, N, dtype;
     size_t esz;
@@ -78,20 +79,19 @@ tm_status make_lin_geo(const tm_shape* s, const tm_linear_w* w, LinGeo* g) {
     if (w->act < TM_ACT_NONE || w->act > TM_ACT_SILU) return TM_ERR_INVALID_ARG;
     if (!al16(w->w) || (w->bias && !al16(w->bias))) return TM_ERR_INVALID_ARG;
     if ((long long)s->B * w->banks > (1LL << 28)) return TM_ERR_UNSUPPORTED;
+    // columns are 32-bit integers, rounded up to a tile's (and a row of x or y across the banks is a tensor-map
+    // stride, below 2^40 bytes)
+    if ((long long)w->banks * w->width > kLinMostCols || (long long)w->banks * w->out > kLinMostCols)
+        return TM_ERR_UNSUPPORTED;
     if (s->dtype == TM_BF16) {
         if (w->width % 8 || w->out % 8) return TM_ERR_UNSUPPORTED;   // 16-byte strides of the tensor maps
-        // a row of x or y across the banks is a tensor-map stride (below 2^40 bytes) and tiles are
-        // counted in 32 bits
-        if ((long long)w->banks * w->width > INT32_MAX || (long long)w->banks * w->out > INT32_MAX)
-            return TM_ERR_UNSUPPORTED;
+        // tiles are counted in 32 bits
         auto t = [](long long v) { return (v + 127) / 128; };
         if ((long long)w->banks * t(s->B) * t(w->out) > (1 << 26) || (long long)w->banks * t(s->B) * t(w->width) > (1 << 26) ||
             (long long)w->banks * t(w->out) * t(w->width) > (1 << 26))
             return TM_ERR_UNSUPPORTED;
     } else {
         if (w->banks > 65535 || (s->B + 63) / 64 > 65535 || (w->out + 63) / 64 > 65535) return TM_ERR_UNSUPPORTED;
-        if ((long long)w->banks * w->width > INT32_MAX || (long long)w->banks * w->out > INT32_MAX)
-            return TM_ERR_UNSUPPORTED;
     }
     g->B = s->B;
     g->banks = w->banks;
