@@ -1,5 +1,6 @@
 """GPU tests of the per-token linear layer's activations and slopes over every finite pre-activation of bf16 (each of the 65280
-values, in bf16 and as fp32), through identity weights, against the float64 oracle.
+values, in bf16 and as fp32), through identity weights, against the float64 oracle; and of rows whose mean is large
+against their spread.
 
 The bounds, derived before any run; h is half a step of the storage type relative to the value:
 
@@ -23,6 +24,7 @@ import torch
 
 from oracle import postnorm as P
 from postnorm_util import DEV, DT, HALF, U, check, f64
+from token_sparse_moe_b200 import _abi as A
 from token_sparse_moe_b200 import api
 
 pytestmark = pytest.mark.gpu
@@ -98,3 +100,20 @@ def test_slope_of_gelu_keeps_its_precision_in_the_tail(dtype, save):
     want = P.act_slope(z, "gelu")
     t = np.where(z <= -1.5, {"bf16": 2e-4, "f32": 1e-4}[dtype], np.inf) * np.abs(want) + 2.0 ** -123
     check("gelu", dz, want, t + HALF[dtype] * (np.abs(want) + t))
+
+
+@pytest.mark.parametrize("width", [45, 384, 1000, 3000])
+def test_rows_of_a_large_mean_from_the_checkpoint(width):
+    """Values of 100 and, one in 16, 101 (exact in the checkpoint): the mean is 400 standard deviations.  With one row dgain
+    is dy n, n = (z - mean) rstd: a subtraction, two products and, in fp32, nothing else to round: 4 u of it."""
+    rng = np.random.default_rng(width)
+    zo = 100.0 + (rng.random((1, 1, width)) < 1 / 16)
+    zo[0, 0, 0] = 101.0
+    do = rng.normal(size=zo.shape).astype(np.float32).astype(np.float64)
+    z, dy = (torch.from_numpy(v).float().to(DEV) for v in (zo, do))
+    sh = api.shape(1, 1, width, 1, "f32", 1e-6)
+    _, saved = api.layer_norm(z, None, A.TM_LAYOUT_ROWS, sh, checkpoint8=True)
+    assert torch.equal(api.checkpoint8_unpack(saved.ckpt), z)
+    _, _, grads = api.layer_norm_backward(dy, saved, A.TM_LAYOUT_ROWS, sh)
+    want = P.layer_norm_backward(zo, do, None, f64(saved.mean), f64(saved.rstd))["dgain"]
+    check("dgain", grads["dgain"], want, 4 * U * np.abs(want) + 1e-30)

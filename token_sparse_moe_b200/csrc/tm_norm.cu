@@ -282,11 +282,12 @@ struct NormRow {
     // n = (z - mu) rs of vector i (columns past the row give values that are not used)
     __device__ __forceinline__ void normalised(int i, float mu, float rs, float2 (&n)[NP]) const {
         if constexpr (CK) {
-            // code * (2^e rs) - mu rs: the code is an integer, its scale exact, one rounding each
+            // code * 2^e is exact, so z - mu is rounded once, whatever the mean (code * (2^e rs) - mu rs, a
+            // multiplication less, is off by |mu| rs roundings)
             ck8_codes<V>(q[i], n);
-            const float a = ck8_scale(e[i]) * rs;
+            const float a = ck8_scale(e[i]);
 #pragma unroll
-            for (int k = 0; k < NP; ++k) n[k] = fma2(n[k], f2(a), f2(-mu * rs));
+            for (int k = 0; k < NP; ++k) n[k] = mul2(fma2(n[k], f2(a), f2(-mu)), f2(rs));
         } else {
             float2 r[NP];
             xw[i].get(n);
