@@ -38,21 +38,23 @@ __device__ __forceinline__ float2 act_slope2(float2 z) {
         return make_float2(f(z.x), f(z.y));
     }
     if constexpr (ACT == LIN_GELU) {
-        // gelu'(-a) = Q(a) - a phi(a) = 1 - gelu'(a) = exp(-a^2 / 2) U(a), a >= 0, with U(a) = M(a) - a / sqrt(2 pi)
-        // and M(a) = Q(a) / exp(-a^2 / 2) a polynomial of degree 4 in t = 1 / (1 + p a), the form of Abramowitz and
-        // Stegun's 26.2.17, fitted here towards the smallest maximum of the absolute error up to a = 1.5 and of U's
+        // gelu'(-a) = Q(a) - a phi(a) = 1 - gelu'(a) = exp(-a^2 / 2) (M(a) - a / sqrt(2 pi)), a >= 0, with
+        // M(a) = Q(a) / exp(-a^2 / 2) a polynomial of degree 4 in r = 1 / (1 + p a), the form of Abramowitz and
+        // Stegun's 26.2.17, fitted here towards the smallest maximum of the absolute error up to a = 1.5 and of the
         // relative one from there to 13.5: 1.5e-6 absolutely, and in the negative tail 1.5e-4 of the slope itself, as
-        // far as exp(-a^2 / 2) is a normal number.  (A polynomial in a alone takes degree 9 and more for that.)  a is
-        // held at 16, where the exponential (of z itself, so that NaN stays) is 0 already and U still finite.
-        const float2 a = make_float2(fminf(fabsf(z.x), 16.f), fminf(fabsf(z.y), 16.f));
-        const float2 x = mul2(mul2(z, z), f2(-0.72134752044448170f));       // -a^2 / 2 in powers of two
-        float2 u = fma2(a, f2(0.429772824f), f2(1.f));
+        // far as exp(-a^2 / 2) is a normal number.  (A polynomial in a alone takes degree 9 and more for that.)
+        // a' = -a sqrt(log2(e) / 2) makes the exponent -a'^2, and with M in units of the factor of a' the sum needs no
+        // product: exp2(-(a'^2 + c)) (2^c M + a'), 2^-c = sqrt(ln 2 / pi).  Past the normal numbers the
+        // exponential is 0 and the sum finite; of a NaN or an infinity the slope is NaN.
+        const float2 a = make_float2(-0.8493218f * fabsf(z.x), -0.8493218f * fabsf(z.y));
+        const float2 x = fma2(a, a, f2(1.09013125f));
+        float2 u = fma2(a, f2(-0.50601883f), f2(1.f));
         const float2 r = make_float2(rcp_approx(u.x), rcp_approx(u.y));
-        u = fma2(f2(-1.19295301e-1f), r, f2(3.51687245e-1f));
-        u = fma2(u, r, f2(8.25978871e-2f));
-        u = fma2(u, r, f2(1.85008666e-1f));
-        u = fma2(u, r, mul2(a, f2(-0.39894228040143268f)));
-        const float2 t = mul2(u, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+        u = fma2(f2(-0.253971815f), r, f2(0.748718917f));
+        u = fma2(u, r, f2(0.175845459f));
+        u = fma2(u, r, f2(0.393871248f));
+        u = fma2(u, r, a);
+        const float2 t = mul2(u, make_float2(ex2_approx(-x.x), ex2_approx(-x.y)));
         return make_float2(z.x < 0.f ? t.x : 1.f - t.x, z.y < 0.f ? t.y : 1.f - t.y);
     }
     if constexpr (ACT == LIN_SILU) {
