@@ -113,7 +113,10 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // Upper tail of the normal distribution, Q(a) = erfc(a / sqrt 2) / 2, a >= 0, for results that are
 // rounded to bf16: log2 Q is nearly a parabola, so a polynomial of degree 5 (fitted to log2 Q on
 // [0, 6] by weighted least squares towards the smallest maximum) and one exponential give Q to a
-// relative 3.7e-4, a fifth of bf16's half step; past 6, where Q < 1e-9, it falls on monotonically.
+// relative 3.7e-4, a tenth of bf16's half step.  Past 6, where Q < 1e-9, it falls on monotonically and too fast: 0.5 %
+// short at 6.5, 2 % at 7, 9 % at 8, nearly all from 12 on.  (A polynomial of degree 7 holds 2.5e-3 as far as Q is a normal
+// number, for two multiply-adds a pair that the epilogue of a short contraction shows: 56 -> 59 us for 16 banks of
+// 4096 x 256 -> 1024.)
 __device__ __forceinline__ float2 gauss_tail2(float2 a) {
     float2 p = make_float2(-2.01684350e-4f, -2.01684350e-4f);
     p = __ffma2_rn(p, a, make_float2(4.46760561e-3f, 4.46760561e-3f));
