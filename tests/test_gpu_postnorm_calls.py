@@ -71,3 +71,14 @@ def test_checkpoint_of_the_widest_rows(width):
         want = api.checkpoint8_pack(x[:, a:b].clone())       # (blocks of 32 are the same ones: step is a multiple)
         assert torch.equal(ck.codes[:, a:b], want.codes) and torch.equal(ck.exps[:, a // 32:(b + 31) // 32], want.exps)
         assert torch.equal(back[:, a:b], api.checkpoint8_unpack(want))
+
+
+def test_a_refused_packing_leaves_the_checkpoint_as_it_was():
+    kept = torch.ones(4, 64, dtype=torch.float32, device=DEV)
+    ck = api.checkpoint8_pack(kept)
+    for x in (torch.ones(5, 64, dtype=torch.bfloat16, device=DEV), torch.ones(64, 4, dtype=torch.bfloat16, device=DEV).t()):
+        with pytest.raises(ValueError):
+            api.checkpoint8_pack(x, out=ck)
+        assert ck.dtype == torch.float32 and torch.equal(api.checkpoint8_unpack(ck), kept)
+    other = api.checkpoint8_pack(torch.full((4, 64), 2.0, dtype=torch.bfloat16, device=DEV), out=ck)
+    assert other is ck and ck.dtype == torch.bfloat16 and torch.equal(api.checkpoint8_unpack(ck).float(), 2 * kept)

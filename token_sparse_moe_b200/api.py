@@ -937,12 +937,12 @@ def checkpoint8_pack(x: torch.Tensor, out: Optional[Checkpoint8] = None, stream=
     shape_ = x.shape
     if out is None:
         out = Checkpoint8.like(x, shape_)
-    out.dtype = x.dtype
     width = shape_[-1]
     st = A.load().tm_checkpoint8_pack(_arg("x", x, shape_, x.dtype, dev), _DT[x.dtype], x.numel() // max(width, 1), width,
                                       out.c("out", shape_, dev), _stream_of(None, dev))
     if st:
         A.check(st, "tm_checkpoint8_pack")
+    out.dtype = x.dtype
     return out
 
 
