@@ -128,10 +128,9 @@ __device__ __forceinline__ float2 gauss_tail2(float2 a) {
 }
 
 // Two activations.  gelu(z) = z Phi(z) = max(z, 0) - |z| Q(|z|): both terms keep their relative
-// precision in the negative tail.  silu(z) = z / (1 + e^-z) for z >= 0 and z e^z / (1 + e^z) below, from t = e^-|z|:
-// the denominators are between 1 and 2, so that one reciprocal of the product of two serves both, and a
-// value depends on its neighbour's by a rounding at most (a NaN's exponential is 0 there).  t below 2^-126 is 0: silu is
-// below 2^-119 there.  NaN comes out as NaN, +inf as +inf, -inf as -0 or 0 (relu, gelu) or NaN (silu: inf / inf).
+// precision in the negative tail.  silu(z) = z / (1 + e^-z), a reciprocal a value: where e^-z is
+// infinite, or its reciprocal no normal number (z < -87, silu below 2^-119), silu is -0.  NaN comes out as NaN, +inf as
+// +inf, -inf as -0 or 0 (relu, gelu) or NaN (silu: inf / inf).
 template <int ACT>
 __device__ __forceinline__ float2 lin_act2(float2 z) {
     if constexpr (ACT == LIN_RELU) return make_float2(max_nan(z.x, 0.f), max_nan(z.y, 0.f));
@@ -141,11 +140,9 @@ __device__ __forceinline__ float2 lin_act2(float2 z) {
         return make_float2(fmaf(-a.x, q.x, max_nan(z.x, 0.f)), fmaf(-a.y, q.y, max_nan(z.y, 0.f)));
     }
     if constexpr (ACT == LIN_SILU) {
-        const float kL = -1.4426950408889634f;   // -log2(e)
-        const float t0 = ex2_approx(fmaxf(kL * fabsf(z.x), -150.f)), t1 = ex2_approx(fmaxf(kL * fabsf(z.y), -150.f));
-        const float d0 = 1.f + t0, d1 = 1.f + t1;
-        const float r = rcp_approx(d0 * d1);
-        return make_float2((z.x >= 0.f ? z.x : z.x * t0) * (r * d1), (z.y >= 0.f ? z.y : z.y * t1) * (r * d0));
+        const float2 x = mul2(z, f2(-1.4426950408889634f));       // -z log2(e)
+        const float2 d = add2(make_float2(ex2_approx(x.x), ex2_approx(x.y)), f2(1.f));
+        return mul2(z, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
     }
     return z;
 }
