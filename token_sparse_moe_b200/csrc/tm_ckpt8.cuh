@@ -75,20 +75,6 @@ struct Pack<__nv_bfloat16, 8> {
     }
 };
 template <>
-struct Pack<__nv_bfloat16, 4> {
-    uint2 w;
-    __device__ __forceinline__ void load(const void* p) { w = __ldg(reinterpret_cast<const uint2*>(p)); }
-    __device__ __forceinline__ void load_shared(const void* p) { w = *reinterpret_cast<const uint2*>(p); }
-    __device__ __forceinline__ void zero() { w = make_uint2(0u, 0u); }
-    __device__ __forceinline__ void get(float2 (&v)[2]) const {
-        v[0] = make_float2(bf16_lo(w.x), bf16_hi(w.x));
-        v[1] = make_float2(bf16_lo(w.y), bf16_hi(w.y));
-    }
-    __device__ __forceinline__ static void store(__nv_bfloat16* p, const float2 (&v)[2]) {
-        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y));
-    }
-};
-template <>
 struct Pack<float, 4> {
     float4 w;
     __device__ __forceinline__ void load(const void* p) { w = __ldg(reinterpret_cast<const float4*>(p)); }
