@@ -484,7 +484,8 @@ TM_API tm_status tm_checkpoint8_unpack(const tm_ckpt8 *in, tm_dtype dtype, size_
 typedef struct { int banks, width; const void *gain, *bias; } tm_layer_norm_w;
 
 /* y = (z - mean) * rstd * gain + bias with z = x_row + residual_row, mean = mean(z), rstd =
- * 1 / sqrt(mean((z - mean)^2) + eps) of each row.
+ * 1 / sqrt(mean((z - mean)^2) + eps) of each row, both in fp32 (where a row's squares overflow it, from deviations of
+ * some 1e19 on, rstd is 0 and y the bias).
  * x: rows, or with TM_LAYOUT_MIXED a token tensor [B, T, D] whose Mix rows are taken (banks = H, width
  * = T * D / H); residual (NULL: none) and y are rows [B, banks, width] in both layouts, so with T = H
  * and residual = X this is the token mixing LN(Mix(X) + X) of [digest] Eq. 5-8.

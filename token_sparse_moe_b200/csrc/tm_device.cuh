@@ -91,7 +91,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
     }
 }
 
-// ------------------------------------------------------------------ TMA (no multicast anywhere)
+// ------------------------------------------------------------------ TMA (no load uses multicast)
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
@@ -357,7 +357,7 @@ __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u 
 }  // namespace tml
 
 namespace tml {
-// ------------------------------------------------------------------ CTA pairs (2-SM MMA), no multicast
+// ------------------------------------------------------------------ CTA pairs (2-SM MMA); no load uses multicast
 __device__ __forceinline__ uint32_t cluster_ctarank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));

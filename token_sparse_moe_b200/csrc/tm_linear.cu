@@ -69,8 +69,9 @@ __device__ __forceinline__ float2 act_slope2(float2 z) {
 // dy, z, dz are [B, cols] with cols = banks * N; a thread owns V columns and walks down its block's
 // rows; the sums over a block's rows go to part [gridDim.y][cols] (in a fixed order).  SRC: what z is
 // read from.  dz may be NULL (no activation: dz is dy, only the sums are wanted).
-// One pass, bound by memory: 8192 x 48 x 1536 bf16 with z whole 562 us (6.4 TB/s); from the checkpoint 513
-// to 600 (a sixth fewer bytes, but the codes' conversion and the slope then take as long as the bus).
+// One pass, bound by memory: 8192 x 48 x 1536 bf16 with z whole 562 us with silu (6.4 TB/s), 585 with gelu; from the
+// checkpoint 500 and 523 (a sixth fewer bytes, but the codes' conversion and the slope then take as long as the bus);
+// under the power cap, between the two contractions, 590 to 620 and 620 to 680.
 // dz is rounded to bf16, the operand type of both contractions that read it: its half step, 2^-8, is of the
 // size of the one in y and dominates the error of dx and dw.
 enum ZSrc : int { Z_NONE = 0, Z_FULL = 1, Z_CK8 = 2 };

@@ -22,10 +22,12 @@
 // costs one exponential per element (2048 cycles of the SM's 16 per cycle), which a contraction of depth 256
 // (2048 tensor cycles) just covers; 8 epilogue warps did not keep up with it, 16 do.
 //
-// Measured (gelu): 48 banks of 8192 x 768 -> 1536 795 us, 1168 TFLOP/s (0.70 of the cuBLAS rate measured on
-// this kind of GPU for one square bf16 product, 0.84 of its rate under the power cap; dX 1347, dW 1373
-// TFLOP/s); with z kept 920, with its checkpoint 943.  8 banks of 4096 x 768 -> 1536 74 us, 16 of 4096 x 256 ->
-// 1024 57 us, where 27 would move the bytes: a tile is 4 slabs, and its 16 warps' epilogue as long as its loads.
+// Measured, calls back to back: 48 banks of 8192 x 768 -> 1536, gelu 755 to 800 us as the power cap allows, 1160 to
+// 1230 TFLOP/s (0.70 to 0.74 of the cuBLAS rate measured on this kind of GPU for one square bf16 product), with z kept
+// 985 to 1030, with its checkpoint 995 to 1100; silu 760 to 780.  8 banks of 4096 x 768 -> 1536: gelu 72 us (1080
+// TFLOP/s), silu 67, z kept or its checkpoint 84, dX 65, dW 59 (1320).  16 banks of 4096 x 256 -> 1024: gelu 48 us with the
+// operands in the L2 and 47 without, where 27 would move the bytes: a tile is 4 slabs, and its 16 warps' epilogue as long
+// as its loads; silu, with a second special function a value, 49, z kept 72, its checkpoint 77.
 #pragma once
 #include "tm_ckpt8.cuh"
 #include "tm_gemm.cuh"

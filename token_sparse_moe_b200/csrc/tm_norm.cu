@@ -11,9 +11,10 @@
 // lanes idle), a warp up to 1024 columns, 4 to 16 warps beyond.  Grids are persistent: gain and bias sit in
 // shared memory as fp32, the sums of dgain and dbias in registers, and the next row's loads are in flight
 // while a row is worked on.  What is then left to bound them is the issue of instructions as much as memory
-// (see tm_ckpt8.cuh): the arithmetic is in pairs throughout.  4096 x 16 rows of 1024 bf16 with a residual:
-// forward 66 us (6.1 TB/s), with the checkpoint 88 (quantising is as much arithmetic as the norm); backward
-// from x and the residual 91 (5.9 TB/s), from the checkpoint 71 (4.8).
+// (see tm_ckpt8.cuh): the arithmetic is in pairs throughout.  4096 x 16 rows of 1024 bf16 with a residual, nothing
+// in the L2 (kernels alone): forward 61 us (6.6 TB/s), with the checkpoint 78 (quantising is as much arithmetic as the
+// norm); backward from x and the residual 100 (5.4 TB/s), from the checkpoint 78 (4.3).  Rows of the Mix view with a
+// residual of their own, 4096 x 48 x 768 (pieces of 16 columns): forward 140, backward 288, from the checkpoint 192.
 // Statistics are two passes over the registers in fp32 (the mean first, then the centred squares): the
 // one-pass form sum(z^2) - mean^2 loses the variance of rows whose mean is large.
 #include <atomic>
@@ -650,9 +651,12 @@ __global__ void __launch_bounds__(NW * 32 + 32, NV <= 2 ? 3 : 1)
 // L2, where the first's copy has just come from, so that the next dy is on its way meanwhile: with dy kept
 // in its slot to the end, two samples of 73 KB do not fit, and a third of the time went by waiting for the
 // next one.  Every warp issues some of a sample's row copies (all of them take one warp some 4000 cycles).
-// Bf16: 8192 x 32 x 512 202 us (4.0 TB/s), 4096 x 48 x 768 227; from the checkpoint 253 and 294.  Not the bus
+// Bf16: 8192 x 32 x 512 205 us (3.9 TB/s), 4096 x 48 x 768 235; from the checkpoint 257 and 296.  Not the bus
 // but a sample's two steps bound it, with a barrier after each and 16 warps an SM: the sums of dgain and dbias
-// stay in 32 to 64 registers a thread, and more warps (20 or 24) spilled and took 310 to 400.
+// stay in 32 to 64 registers a thread, and more warps (20 or 24) spilled and took 310 to 400.  So the checkpoint, a
+// sixth fewer bytes but its codes converted in both steps, saves memory here and costs time.  Fp32: 4096 x 32 x 512 152
+// us, from the checkpoint 183; samples of 48 x 768 do not fit three slots and take ln_bwd_self_kernel, 2048 of them
+// 432, and 250 from the checkpoint, without the scattered reads of x.
 // Dynamic shared memory: 3 slots, gain, and per row of a slot its constants, statistics and sums.
 template <typename T, int NV, bool CK, int NW>
 __global__ void __launch_bounds__(NW * 32, NW <= 12 ? 2 : 1)

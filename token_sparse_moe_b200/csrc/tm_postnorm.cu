@@ -135,7 +135,8 @@ bool map_mats_f32(CUtensorMap* m, const void* base, uint64_t mats, int R, int W)
 // a pair's 256 x 256 tile (about 512 tensor-core cycles): full waves of tiles times slabs, plus a tile's
 // fill and epilogue.  A 128 x 128 tile does a quarter of the work on half the SMs: its slab takes 0.6 of a
 // pair's, bound by its loads (as many bytes per SM), or 0.95 where both operands come in 64-row boxes (dW);
-// a split adds the partial sums' way out and back through memory and one more launch.  Measured, pair / tile:
+// a split adds the partial sums' way out and back through memory and one more launch.  Measured (gelu, twenty kernels
+// in a row in a graph, operands in the L2 where they fit), pair / tile:
 // forward 16 banks of 4096 x 256 -> 1024 45 / 53 us, 8 of 4096 x 768 -> 1536 71 / 90, 4 of 1000 x 512 -> 512
 // 11.2 / 8.3, 16 of 333 x 384 -> 264 11.2 / 8.2; dW of 8 x 3829 x 168 x 600 as 1 / 2 / 3 / 4 runs 40 / 26 / 21 / 28,
 // of 48 x 1419 x 888 x 568 99 / 156 / 187 / 215.  Over 60 random dW the choice is 1.7 % above the best of all.
