@@ -4,9 +4,9 @@ against their spread.
 
 The bounds, derived before any run; h is half a step of the storage type relative to the value:
 
-* bf16 silu, z < 0: its exponential is e^-|z|, whose exponent of up to 126 in fp32 with two roundings is off by
-  2 * 126 * 2^-24 = 1.5e-5; the exponential, the reciprocal and five steps (2^-20): 2e-4 of the value, as far as the
-  exponential is a normal fp32 number (2^-126).  Below that it is taken as 0: silu is at most 90 * 2^-126 < 2^-119 there.
+* bf16 silu, z < 0: e^-z, whose exponent of up to 127 in fp32 with two roundings is off by 2 * 127 * 2^-24 = 1.5e-5;
+  the exponential, the reciprocal and five steps (2^-20): 2e-4 of the value, as far as the reciprocal is a normal fp32
+  number (2^-126).  Below that it is taken as 0: silu is at most 90 * 2^-126 < 2^-119 there.
 * bf16 gelu, z < 0: the documented 3.7e-4 of the tail up to 6, an exponent of up to 30 there in fp32 with six roundings
   (6 * 30 u ln 2 = 8e-6), the exponential and two steps: 4.5e-4.  Past 6 the tail is documented to fall short by up to all
   of it: an absolute 6e-9 at most.
@@ -31,7 +31,7 @@ from token_sparse_moe_b200 import _abi as A
 from token_sparse_moe_b200 import api
 
 pytestmark = pytest.mark.gpu
-GONE = 2.0 ** -119                        # what an exponential below the normal fp32 numbers may have held
+GONE = 2.0 ** -119                        # what a tail below the normal fp32 numbers may have held
 
 
 def every_value(order):
